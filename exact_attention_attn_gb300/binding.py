@@ -72,6 +72,22 @@ def load_library() -> ctypes.CDLL:
         lib.attn_bwd.restype = ci
         lib.attn_fwd_host.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, cf, ci, vp]
         lib.attn_fwd_host.restype = ci
+        lib.attn_rope_table.argtypes = [vp, vp, ci, ci, vp]
+        lib.attn_rope_table.restype = ci
+        lib.attn_rope.argtypes = [vp, vp, vp, vp, ci] * 2 + [vp, ll, ll, ci, vp] + [ci] * 6 + [vp]
+        lib.attn_rope.restype = ci
+        lib.attn_pages_assign.argtypes = [vp, ll, ci, vp, vp, ci, ci, vp, ci, vp, vp, vp, vp, vp, vp, ci, vp, vp]
+        lib.attn_pages_assign.restype = ci
+        lib.attn_pages_release.argtypes = [vp, ll, ci, vp, vp, ci, ci, vp, ci, vp, vp, vp, vp, vp]
+        lib.attn_pages_release.restype = ci
+        lib.attn_kv4_page_bytes.argtypes = [ci, ci]
+        lib.attn_kv4_page_bytes.restype = ll
+        lib.attn_kv4_append.argtypes = [vp, ll, ll, vp, ll, ll, vp, vp, ci, ci, ci, ci, ci, vp]
+        lib.attn_kv4_append.restype = ci
+        lib.attn_kv4_read.argtypes = [vp, ci, vp, vp, ll, ll, vp, ll, ll, ci, ci, ci, ci, vp]
+        lib.attn_kv4_read.restype = ci
+        lib.attn_fwd_kv4.argtypes = [vp, ll, ll, vp, vp, vp, ll, ci, vp, ci, vp, vp] + [ci] * 6 + [cf, ci, vp]
+        lib.attn_fwd_kv4.restype = ci
         lib.attn_set_debug.argtypes = [ci, ctypes.c_longlong]
         lib.attn_set_debug.restype = ci
         lib.attn_fwd_status.argtypes = [vp]

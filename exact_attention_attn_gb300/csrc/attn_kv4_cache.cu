@@ -1,0 +1,274 @@
+// The 4-bit KV cache: quantising tokens into their slots, and reading slots
+// back as bfloat16.
+//
+// Per token, kv head and 64 dims:  m = min x,  s = bf16((max x - m) / 15),
+// c = rint((x - m) / s) in 0 .. 15 (0 where s = 0); the cache holds c in four
+// bits and (s, m) as bfloat16.  m is one of the bfloat16 inputs, so it is
+// held exactly; s is rounded to nearest once.  A group that holds an infinity
+// or a NaN gets s = m = NaN, so that attention over it is NaN as it would be
+// over the unquantised values.
+//
+// The differences are formed on x / 16, so that max - min of finite values
+// stays finite; the factor is a power of two and leaves every result alone.
+// The quotient is rounded as a division would round it, from one reciprocal
+// of the group's scale and a residual (q0 = d r, q = q0 + (d - q0 s) r), three
+// operations instead of a division's ten; groups whose scale is so small or
+// large that these could leave the normal range divide.
+//
+// Eight threads share a group (16 bytes of bfloat16 each, one 4-byte word of
+// codes); 32 consecutive tokens share a CTA, so that a warp writes four
+// neighbouring rows and pairs.  Bound: HBM, 2 + 0.5625 bytes a value.
+#include <cuda_bf16.h>
+#include <math.h>
+#include <string.h>
+
+#include "attn.h"
+#include "attn_internal.h"
+#include "attn_kv4.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTokens = kThreads / 8;  // tokens of a CTA
+
+struct AppendParams {
+  const __nv_bfloat16 *k, *v;
+  int64_t kt, kh, vt, vh;  // element strides of token and head
+  const int *slots;
+  uint8_t *cache;
+  int64_t nslots;
+  int T, H, G, shift;
+  int *status;
+};
+
+// Codes and pair of one group of 64 values, 8 of them (w) in each of 8 lanes.
+__device__ __forceinline__ void quantise8(const uint4 &w, uint32_t &codes, uint32_t &pair) {
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+  __nv_bfloat162 h[4];
+  memcpy(h, ws, sizeof(ws));
+  // minimum and maximum of the lane's values, NaN where there is one
+  __nv_bfloat162 lo2 = __hmin2_nan(__hmin2_nan(h[0], h[1]), __hmin2_nan(h[2], h[3]));
+  __nv_bfloat162 hi2 = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+  __nv_bfloat162 a = __halves2bfloat162(__low2bfloat16(lo2), __hneg(__low2bfloat16(hi2)));
+  __nv_bfloat162 b = __halves2bfloat162(__high2bfloat16(lo2), __hneg(__high2bfloat16(hi2)));
+  __nv_bfloat162 r = __hmin2_nan(a, b);  // (min, -max): one minimum reduces both
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    uint32_t u;
+    memcpy(&u, &r, 4);
+    u = __shfl_xor_sync(0xffffffffu, u, o);
+    __nv_bfloat162 t;
+    memcpy(&t, &u, 4);
+    r = __hmin2_nan(r, t);
+  }
+  const float lo = __low2float(r) * 0.0625f, hi = -__high2float(r) * 0.0625f;
+  const __nv_bfloat16 sb = __float2bfloat16_rn((hi - lo) / 0.9375f);  // ((max - min) / 16) / (15 / 16)
+  const float s = __bfloat162float(sb) * 0.0625f;
+  uint16_t sbits, mbits;
+  memcpy(&sbits, &sb, 2);
+  const __nv_bfloat16 mb = __low2bfloat16(r);
+  memcpy(&mbits, &mb, 2);
+  codes = 0;
+  if (!(hi - lo < INFINITY)) {
+    pair = 0x7fff7fffu;  // NaN, NaN
+    return;
+  }
+  pair = sbits | ((uint32_t)mbits << 16);
+  if (s == 0.f) return;
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number, ties to even
+  float q[8];
+  const bool divide = s < 0x1p-90f || s > 0x1p90f;
+  const float inv = 1.f / s;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x0 = __uint_as_float(ws[i] << 16), x1 = __uint_as_float(ws[i] & 0xffff0000u);
+    const float d0 = fmaf(x0, 0.0625f, -lo), d1 = fmaf(x1, 0.0625f, -lo);
+    float q0 = d0 * inv, q1 = d1 * inv;
+    q0 = fmaf(fmaf(-q0, s, d0), inv, q0);
+    q1 = fmaf(fmaf(-q1, s, d1), inv, q1);
+    if (divide) {
+      q0 = d0 / s;
+      q1 = d1 / s;
+    }
+    q[2 * i] = q0;
+    q[2 * i + 1] = q1;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t t = __float_as_uint(fminf(q[i], 15.f) + kMagic) & 15u;
+    codes |= t << (4 * i);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) attn_kv4_append_kernel(const AppendParams p) {
+  const int t = blockIdx.x * kTokens + (threadIdx.x >> 3), sub = threadIdx.x & 7;
+  int slot = t < p.T ? p.slots[t] : -1;
+  if (slot >= p.nslots || slot < -1) {  // no such slot: not written
+    atomicCAS(p.status, 0, kStatusDevice);
+    slot = -1;
+  }
+  const int P = 1 << p.shift;
+  const int64_t page_bytes = kv4_page_bytes(p.G, P), side = kv4_side_bytes(p.G, P);
+  const int row = slot & (P - 1);
+  uint8_t *page = p.cache + (int64_t)(slot >> p.shift) * p.H * page_bytes;
+  // lanes without a slot stay for the shuffles and read their warp's values nowhere
+  for (int hg = blockIdx.y; hg < p.H * p.G; hg += gridDim.y) {
+    const int h = hg / p.G, g = hg - h * p.G;
+    uint4 wk = make_uint4(0, 0, 0, 0), wv = wk;
+    if (slot >= 0) {
+      wk = *reinterpret_cast<const uint4 *>(p.k + (int64_t)t * p.kt + (int64_t)h * p.kh + g * kKv4Group + sub * 8);
+      wv = *reinterpret_cast<const uint4 *>(p.v + (int64_t)t * p.vt + (int64_t)h * p.vh + g * kKv4Group + sub * 8);
+    }
+    uint32_t ck, pk, cv, pv;
+    quantise8(wk, ck, pk);
+    quantise8(wv, cv, pv);
+    if (slot < 0) continue;
+    uint8_t *at = page + (int64_t)h * page_bytes + ((int64_t)g * P + row) * kKv4RowBytes + sub * 4;
+    uint8_t *pairs = page + (int64_t)h * page_bytes + kv4_codes_bytes(p.G, P) + ((int64_t)g * P + row) * kKv4PairBytes;
+    *reinterpret_cast<uint32_t *>(at) = ck;
+    *reinterpret_cast<uint32_t *>(at + side) = cv;
+    if (sub == 0) {
+      *reinterpret_cast<uint32_t *>(pairs) = pk;
+      *reinterpret_cast<uint32_t *>(pairs + side) = pv;
+    }
+  }
+}
+
+struct ReadParams {
+  const uint8_t *cache;
+  const int *slots;
+  __nv_bfloat16 *k, *v;
+  int64_t kh, kt, vh, vt;  // element strides of head and token
+  int64_t nslots;
+  int T, H, G, shift;
+  int *status;
+};
+
+__device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t pair) {
+  const float s = __uint_as_float(pair << 16), m = __uint_as_float(pair & 0xffff0000u);
+  __nv_bfloat162 h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float c0 = (float)((codes >> (8 * i)) & 15u), c1 = (float)((codes >> (8 * i + 4)) & 15u);
+    h[i] = __floats2bfloat162_rn(fmaf(c0, s, m), fmaf(c1, s, m));  // c * s is exact: one rounding, then bfloat16's
+  }
+  uint4 w;
+  memcpy(&w, h, sizeof(w));
+  return w;
+}
+
+__global__ void __launch_bounds__(kThreads) attn_kv4_read_kernel(const ReadParams p) {
+  const int t = blockIdx.x * kTokens + (threadIdx.x >> 3), sub = threadIdx.x & 7;
+  if (t >= p.T) return;
+  int slot = p.slots[t];
+  if (slot >= p.nslots || slot < -1) {
+    atomicCAS(p.status, 0, kStatusDevice);
+    slot = -1;
+  }
+  const int P = 1 << p.shift;
+  const int64_t page_bytes = kv4_page_bytes(p.G, P), side = kv4_side_bytes(p.G, P);
+  const int row = slot & (P - 1);
+  const uint8_t *page = p.cache + (int64_t)(slot >> p.shift) * p.H * page_bytes;
+  for (int hg = blockIdx.y; hg < p.H * p.G; hg += gridDim.y) {
+    const int h = hg / p.G, g = hg - h * p.G;
+    uint4 wk = make_uint4(0, 0, 0, 0), wv = wk;
+    if (slot >= 0) {
+      const uint8_t *at = page + (int64_t)h * page_bytes + ((int64_t)g * P + row) * kKv4RowBytes + sub * 4;
+      const uint8_t *pairs =
+          page + (int64_t)h * page_bytes + kv4_codes_bytes(p.G, P) + ((int64_t)g * P + row) * kKv4PairBytes;
+      const uint32_t ck = *reinterpret_cast<const uint32_t *>(at), cv = *reinterpret_cast<const uint32_t *>(at + side);
+      const uint32_t pk = *reinterpret_cast<const uint32_t *>(pairs), pv = *reinterpret_cast<const uint32_t *>(pairs + side);
+      wk = values8(ck, pk);
+      wv = values8(cv, pv);
+    }
+    *reinterpret_cast<uint4 *>(p.k + (int64_t)h * p.kh + (int64_t)t * p.kt + g * kKv4Group + sub * 8) = wk;
+    *reinterpret_cast<uint4 *>(p.v + (int64_t)h * p.vh + (int64_t)t * p.vt + g * kKv4Group + sub * 8) = wv;
+  }
+}
+
+bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+// The checks append and read share.
+int check_cache(const void *cache, int num_pages, int H, int D, int P, int T, const int *slots) {
+  if (num_pages < 0 || T < 0 || H < 1 || H > 65535 || kv4_page_shift(P) < 0) return ATTN_ERR_ARG;
+  if (D < 64 || D > ATTN_MAX_HEAD_DIM || D % 64 != 0) return ATTN_ERR_ARG;
+  if ((int64_t)num_pages * P > 0x7fffffffLL) return ATTN_ERR_ARG;  // slots are 32-bit
+  if (T == 0) return ATTN_OK;
+  if (!slots || (num_pages > 0 && !cache)) return ATTN_ERR_ARG;
+  if (off16(cache) || (reinterpret_cast<uintptr_t>(slots) & 3u)) return ATTN_ERR_ALIGN;
+  return ATTN_OK;
+}
+
+// Strides of one [T, H, D] view.
+int check_view(const void *x, long long t, long long h) {
+  if (!x || t < 0 || h < 0) return ATTN_ERR_ARG;
+  return off16(x) || t % 8 || h % 8 ? ATTN_ERR_ALIGN : ATTN_OK;
+}
+
+// 32 tokens a CTA; where that leaves SMs idle, the heads' groups are spread
+// over gridDim.y CTAs, two CTAs per SM at most.
+dim3 cache_grid(int T, int HG, int sms) {
+  const int x = (T + kTokens - 1) / kTokens;
+  int y = (2 * sms + x - 1) / x;
+  y = y < 1 ? 1 : y > HG ? HG : y;
+  return dim3((unsigned)x, (unsigned)y);
+}
+
+}  // namespace
+}  // namespace attn
+
+extern "C" {
+
+long long attn_kv4_page_bytes(int D, int page_size) {
+  if (D < 64 || D > ATTN_MAX_HEAD_DIM || D % 64 != 0 || attn::kv4_page_shift(page_size) < 0) return ATTN_ERR_ARG;
+  return attn::kv4_page_bytes(D / 64, page_size);
+}
+
+int attn_kv4_append(const void *k, long long k_stride_t, long long k_stride_h, const void *v, long long v_stride_t,
+                    long long v_stride_h, const int *slots, void *cache, int num_pages, int T, int Hkv, int D,
+                    int page_size, attn_stream_t stream) {
+  using namespace attn;
+  int rc = check_cache(cache, num_pages, Hkv, D, page_size, T, slots);
+  if (rc != ATTN_OK || T == 0) return rc;
+  if ((rc = check_view(k, k_stride_t, k_stride_h)) != ATTN_OK) return rc;
+  if ((rc = check_view(v, v_stride_t, v_stride_h)) != ATTN_OK) return rc;
+  int device = 0, sms = 0;
+  AppendParams p{};
+  if ((rc = current_device(&device, &sms, &p.status)) != ATTN_OK) return rc;
+  p.k = static_cast<const __nv_bfloat16 *>(k);
+  p.v = static_cast<const __nv_bfloat16 *>(v);
+  p.kt = k_stride_t; p.kh = k_stride_h; p.vt = v_stride_t; p.vh = v_stride_h;
+  p.slots = slots;
+  p.cache = static_cast<uint8_t *>(cache);
+  p.nslots = (int64_t)num_pages * page_size;
+  p.T = T; p.H = Hkv; p.G = D / 64; p.shift = kv4_page_shift(page_size);
+  attn_kv4_append_kernel<<<cache_grid(T, Hkv * p.G, sms), kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? ATTN_OK : record_cuda_error(e);
+}
+
+int attn_kv4_read(const void *cache, int num_pages, const int *slots, void *k, long long k_stride_h,
+                  long long k_stride_t, void *v, long long v_stride_h, long long v_stride_t, int T, int Hkv, int D,
+                  int page_size, attn_stream_t stream) {
+  using namespace attn;
+  int rc = check_cache(cache, num_pages, Hkv, D, page_size, T, slots);
+  if (rc != ATTN_OK || T == 0) return rc;
+  if ((rc = check_view(k, k_stride_t, k_stride_h)) != ATTN_OK) return rc;
+  if ((rc = check_view(v, v_stride_t, v_stride_h)) != ATTN_OK) return rc;
+  int device = 0, sms = 0;
+  ReadParams p{};
+  if ((rc = current_device(&device, &sms, &p.status)) != ATTN_OK) return rc;
+  p.cache = static_cast<const uint8_t *>(cache);
+  p.slots = slots;
+  p.k = static_cast<__nv_bfloat16 *>(k);
+  p.v = static_cast<__nv_bfloat16 *>(v);
+  p.kh = k_stride_h; p.kt = k_stride_t; p.vh = v_stride_h; p.vt = v_stride_t;
+  p.nslots = (int64_t)num_pages * page_size;
+  p.T = T; p.H = Hkv; p.G = D / 64; p.shift = kv4_page_shift(page_size);
+  attn_kv4_read_kernel<<<cache_grid(T, Hkv * p.G, sms), kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? ATTN_OK : record_cuda_error(e);
+}
+
+}  // extern "C"

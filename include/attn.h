@@ -313,6 +313,176 @@ ATTN_API int attn_fwd_fp8(const void *q8, const void *k8, const void *vt8, const
                           float scale, int causal, attn_stream_t stream);
 
 /*
+ * attn_rope / attn_rope_table -- rotary positions with several axes, the step
+ * before attn_fwd, attn_bwd and the KV cache.
+ *
+ * Frequency i of the first rot dims of every head turns its pair (x1, x2) by
+ * the angle phi = positions[axis_i][b][n] * inv_freq_i:
+ *     y1 = x1 cos(phi) - x2 sin(phi),   y2 = x2 cos(phi) + x1 sin(phi),
+ * the pair being dims (i, i + rot/2), or (2i, 2i + 1) with adjacent = 1.  Dims
+ * from rot on are copied.  backward = 1 turns by -phi, which maps the gradient
+ * of the output to that of the input.  Angles are exact for every int32
+ * position (64-bit fractions of a turn, see attn_rope_table), the rotation is
+ * float32, the output is rounded once.
+ *
+ * q, k   device pointers, bf16; element (b, h, n, d) at b * strides[0] +
+ *        h * strides[1] + n * strides[2] + d.  Strides are host arrays of three
+ *        element counts >= 0, multiples of 8.  q_out and k_out likewise; an
+ *        output may be its own input with the same strides (in place) but must
+ *        not overlap one in another way, and no two of an output's elements
+ *        may share an address.  Hq = 0 or Hkv = 0 leaves that tensor out.
+ * positions  device pointer, int32; axis a of (b, n) at a * pos_stride_axis +
+ *        b * pos_stride_b + n.
+ * axes   1 .. ATTN_ROPE_MAX_AXES.
+ * table  device pointer, rot / 2 entries of attn_rope_table made for at most
+ *        `axes` axes (an entry of another axis is read as axis 0, and
+ *        attn_fwd_status reports ATTN_ERR_DEVICE).
+ * D      a multiple of 64 up to 1024; rot a multiple of 16, 16 .. D.
+ * All base addresses 16-byte aligned (positions: 4).  Asynchronous on
+ * `stream`, one launch, no workspace; may be captured into a CUDA graph.
+ *
+ * attn_rope_table (host only) fills table[2 i] with inv_freq[i] / (2 pi)
+ * modulo 1 as a 64-bit fraction and table[2 i + 1] with axis[i], for i < n <=
+ * 512; inv_freq finite, 0 <= axis[i] < axes.  The caller copies it to the
+ * device once.
+ */
+#define ATTN_ROPE_MAX_AXES 8
+ATTN_API int attn_rope_table(const double *inv_freq, const int *axis, int n, int axes, long long *table);
+ATTN_API int attn_rope(const void *q, const long long *q_strides, void *q_out, const long long *q_out_strides, int Hq,
+                       const void *k, const long long *k_strides, void *k_out, const long long *k_out_strides,
+                       int Hkv, const int *positions, long long pos_stride_axis, long long pos_stride_b, int axes,
+                       const long long *table, int B, int N, int D, int rot, int adjacent, int backward,
+                       attn_stream_t stream);
+
+/*
+ * attn_pages_assign / attn_pages_release -- the pages of a KV cache, handed out
+ * and taken back on the device from request lengths the host need not know.
+ *
+ * State (device, int32): block_table, row r at r * table_stride, entry j the
+ * page of tokens j * page_size ... of request r; lens[B], the tokens each
+ * request holds (in its first ceil(len / page_size) entries); free_pages, a
+ * stack of page ids whose first *free_count entries are free.
+ *
+ * assign adds new_lens[r] tokens to each request: pages from the top of the
+ *   stack, in request order, go into the table behind the ones it has.  It
+ *   writes lens_out = lens + new_lens, free_count_out, cu[B + 1] (first token
+ *   of each request among this step's tokens, and their number), and for each
+ *   of the step's tokens slots (page * page_size + offset) and positions (its
+ *   place in its request); entries from cu[B] to max_tokens become slot -1,
+ *   position 0.  info[0] = 0, info[1] = cu[B].
+ * release shortens request r to keep_lens[r] tokens (a negative value, or one
+ *   not below lens[r], leaves it): the pages behind ceil(keep / page_size) are
+ *   pushed on the stack in request order and their entries become -1.  Writes
+ *   lens_out and free_count_out; info[0] = 0, info[1] = the pages given back.
+ *
+ * Refused as a whole, on the device: info[0] is then an OR of the ATTN_PAGES_*
+ * bits, info[1] = 0, lens_out = lens, free_count_out = *free_count, table and
+ * stack are unchanged, cu is all 0 and every slot -1:
+ *   BAD_LENGTH       a length is negative or past max_pages * page_size;
+ *   TOO_MANY_TOKENS  the step has more than max_tokens tokens;
+ *   NO_FREE_PAGES    more pages are needed than are free (release: more are
+ *                    given back than free_capacity has room for);
+ *   BAD_COUNT        *free_count is not in 0 .. free_capacity.
+ *
+ * lens_out may be lens and free_count_out may be free_count (updates in
+ * place); no other buffers may overlap.  page_size is 16, 32 or 64; B is 0 ..
+ * ATTN_PAGES_MAX_REQUESTS; a row of the table has max_pages entries
+ * (table_stride >= max_pages, max_pages * page_size < 2^31).  Page ids are not
+ * interpreted.  One launch, no workspace, asynchronous on `stream`; may be
+ * captured into a CUDA graph; deterministic.
+ */
+#define ATTN_PAGES_MAX_REQUESTS 16384
+#define ATTN_PAGES_BAD_LENGTH 1
+#define ATTN_PAGES_TOO_MANY_TOKENS 2
+#define ATTN_PAGES_NO_FREE_PAGES 4
+#define ATTN_PAGES_BAD_COUNT 8
+ATTN_API int attn_pages_assign(int *block_table, long long table_stride, int max_pages, const int *lens,
+                               const int *new_lens, int B, int page_size, const int *free_pages, int free_capacity,
+                               const int *free_count, int *lens_out, int *free_count_out, int *cu, int *slots,
+                               int *positions, int max_tokens, int *info, attn_stream_t stream);
+ATTN_API int attn_pages_release(int *block_table, long long table_stride, int max_pages, const int *lens,
+                                const int *keep_lens, int B, int page_size, int *free_pages, int free_capacity,
+                                const int *free_count, int *lens_out, int *free_count_out, int *info,
+                                attn_stream_t stream);
+
+/*
+ * attn_kv4_append / attn_kv4_read -- a KV cache of 4 bits a value.
+ *
+ * The cache is uint8 [num_pages, Hkv, attn_kv4_page_bytes(D, page_size)].  A
+ * page of one kv head holds, with G = D / 64: K's codes [G][page_size][32
+ * bytes] (byte b: dim 2b of the group in the low nibble, 2b + 1 in the high
+ * one), K's pairs [G][page_size][scale, minimum] (bf16), then V's codes and
+ * pairs.  Per token, kv head and 64 dims:
+ *     m = min x,  s = bf16((max x - m) / 15),  c = rint((x - m) / s) in 0..15
+ * (c = 0 where s = 0), and the code stands for s c + m.  Rounding is to
+ * nearest, ties to even.  A group that holds an infinity or a NaN gets s = m =
+ * NaN and codes 0.
+ *
+ * attn_kv4_append writes token t's K and V into slot slots[t] = page *
+ *   page_size + offset.  k and v are bf16, element (t, h, d) at t * stride_t +
+ *   h * stride_h + d.  Slot -1 skips the token; the other slots of a call must
+ *   be distinct (what a slot named twice holds afterwards is unspecified).
+ * attn_kv4_read writes the values that slot slots[t] stands for, rounded to
+ *   bf16, to k and v (element (h, t, d) at h * stride_h + t * stride_t + d): a
+ *   cached prefix for attn_fwd.  Slot -1 reads as zeros; a slot may be read
+ *   more than once.
+ * A slot below -1 or not below num_pages * page_size is treated as -1 and
+ * attn_fwd_status reports ATTN_ERR_DEVICE.
+ *
+ * page_size is 16, 32 or 64; D a multiple of 64 up to 1024; num_pages *
+ * page_size < 2^31.  Strides are element counts >= 0, multiples of 8; base
+ * addresses 16-byte aligned (slots: 4).  Asynchronous on `stream`, one launch,
+ * no workspace; may be captured into a CUDA graph.
+ */
+ATTN_API long long attn_kv4_page_bytes(int D, int page_size);
+ATTN_API int attn_kv4_append(const void *k, long long k_stride_t, long long k_stride_h, const void *v,
+                             long long v_stride_t, long long v_stride_h, const int *slots, void *cache,
+                             int num_pages, int T, int Hkv, int D, int page_size, attn_stream_t stream);
+ATTN_API int attn_kv4_read(const void *cache, int num_pages, const int *slots, void *k, long long k_stride_h,
+                           long long k_stride_t, void *v, long long v_stride_h, long long v_stride_t, int T, int Hkv,
+                           int D, int page_size, attn_stream_t stream);
+
+/*
+ * attn_fwd_kv4 -- exact attention over the 4-bit cache, for requests of any
+ * length with one or a few query tokens each.
+ *
+ * Request r has the query tokens cu[r] .. cu[r + 1] - 1 (nq of them, maybe
+ * none) and lens[r] cached tokens (its own included), in the pages that row r
+ * of block_table names.  For query token i of the request and query head hq,
+ * kv head hq / (Hq / Hkv), over the values the cache stands for:
+ *     S_j = scale * q_i . K_j,  hidden where causal and j > i + lens[r] - nq,
+ *     O = softmax(S) V,  LSE = ln sum_j exp(S_j).
+ * A row that sees no key gets O = 0 and LSE = -inf.
+ *
+ * q      bf16, element (t, h, d) at t * q_stride_t + h * q_stride_h + d.
+ * o      bf16 [T, Hq, D] contiguous; lse fp32 [T, Hq].  Rows of tokens before
+ *        cu[0] or from cu[B] on are left as they were.
+ * cu, lens, block_table  device, int32, as attn_pages_assign makes them.
+ * D      64, 128, 192 or 256.  page_size, num_pages, max_pages, table_stride as
+ *        above.  B is 0 .. ATTN_KV4_MAX_REQUESTS.
+ * scale  finite.  Products are exact on the codes (fp32 accumulation); the
+ *        probabilities are rounded to 11 bits before the second product, O
+ *        once to bf16.
+ * Nothing in a page past a request's last token, and nothing hidden from a
+ * row, reaches that row's result, whatever it holds.  A table entry that is
+ * not in 0 .. num_pages - 1, a length outside 0 .. max_pages * page_size, or
+ * query tokens outside 0 .. T is brought into range (that request's result is
+ * then undefined) and attn_fwd_status reports ATTN_ERR_DEVICE.
+ *
+ * Asynchronous on `stream`: two launches, and a stream-ordered workspace of at
+ * most 2048 * (2 * 16 * (D + 2) * 4 + 32) bytes from the library's pool
+ * (ATTN_ERR_NOMEM if it cannot be had).  CUDA graphs: as attn_fwd; the grid
+ * depends on the sizes alone, so a replay may have other lengths, tables and
+ * query counts.  Deterministic for given lengths on a given device.
+ */
+#define ATTN_KV4_MAX_REQUESTS 16384
+#define ATTN_KV4_MAX_HEAD_DIM 256
+ATTN_API int attn_fwd_kv4(const void *q, long long q_stride_t, long long q_stride_h, const int *cu, const int *lens,
+                          const int *block_table, long long table_stride, int max_pages, const void *cache,
+                          int num_pages, void *o, float *lse, int B, int T, int Hq, int Hkv, int D, int page_size,
+                          float scale, int causal, attn_stream_t stream);
+
+/*
  * attn_fwd_status -- synchronise `stream`, then read and clear the device
  * status word of the current device.  Returns ATTN_OK, ATTN_ERR_TIMEOUT (a
  * bounded mbarrier wait inside a kernel gave up; that kernel's outputs are

@@ -1,0 +1,136 @@
+"""Refusals of the rotary, page, cache and kv4 entry points, without a GPU:
+through the C ABI, and through the binding's own checks."""
+import ctypes as C
+
+import pytest
+import torch
+
+from test_abi import Buf, lib  # noqa: F401  (the built library)
+
+ARG, ALIGN = -1, -2
+
+
+def strides(*s):
+    return (C.c_longlong * 3)(*s)
+
+
+def test_rope_table(lib):  # noqa: F811
+    n = 3
+    out = (C.c_longlong * 6)()
+    freq, axis = (C.c_double * n)(1.0, 0.5, 7.0), (C.c_int * n)(0, 1, 1)
+    assert lib.attn_rope_table(freq, axis, n, 2, out) == 0
+    turns = [(v % (1 << 64)) / 2.0 ** 64 for v in out[0::2]]
+    two_pi = 6.283185307179586
+    for got, f in zip(turns, (1.0, 0.5, 7.0)):
+        assert abs(got - (f / two_pi) % 1.0) < 1e-15
+    assert list(out[1::2]) == [0, 1, 1]
+    assert lib.attn_rope_table((C.c_double * 1)(-1e-30), axis, 1, 2, out) == 0 and out[0] == 0  # a whole turn is none
+    assert lib.attn_rope_table(freq, axis, n, 1, out) == ARG          # an axis past the last
+    assert lib.attn_rope_table((C.c_double * n)(1, float("inf"), 1), axis, n, 2, out) == ARG
+    assert lib.attn_rope_table(freq, axis, 513, 2, out) == ARG
+    assert lib.attn_rope_table(freq, axis, n, 9, out) == ARG
+    assert lib.attn_rope_table(None, axis, n, 2, out) == ARG
+    assert lib.attn_rope_table(None, None, 0, 1, None) == 0
+
+
+def test_rope_refusals(lib):  # noqa: F811
+    p = Buf().p
+    s = strides(512, 64, 256)
+
+    def rope(q=p, qs=s, o=p, os=s, Hq=4, k=None, Hkv=0, pos=p, pa=8, pb=0, axes=1, table=p, B=1, N=2, D=64, rot=64,
+             adj=0, bwd=0):
+        return lib.attn_rope(q, qs, o, os, Hq, k, s, k, s, Hkv, pos, pa, pb, axes, table, B, N, D, rot, adj, bwd, None)
+
+    for bad in (dict(D=96), dict(D=1088), dict(rot=8), dict(rot=24), dict(rot=80), dict(axes=0), dict(axes=9), dict(adj=2),
+                dict(bwd=-1), dict(B=-1), dict(N=-1), dict(Hq=-1), dict(pa=-1), dict(pb=-4), dict(q=None), dict(o=None),
+                dict(qs=None), dict(Hkv=2), dict(pos=None), dict(table=None), dict(qs=strides(512, -64, 256)),
+                dict(os=strides(512, 64, 264))):  # in place with another layout
+        assert rope(**bad) == ARG, bad
+    for bad in (dict(q=p + 2), dict(o=p + 8), dict(qs=strides(512, 68, 256)), dict(os=strides(4, 64, 256)),
+                dict(table=p + 8), dict(pos=p + 2)):
+        assert rope(**bad) == ALIGN, bad
+    assert rope(B=0, q=None) == 0 and rope(N=0, q=None) == 0 and rope(Hq=0, q=None) == 0
+
+
+def test_pages_refusals(lib):  # noqa: F811
+    p = Buf().p
+
+    def assign(table=p, stride=8, width=8, lens=p, new=p, B=2, P=16, free=p, cap=4, count=p, lo=p, co=p, cu=p, slots=p,
+               pos=p, most=4, info=p):
+        return lib.attn_pages_assign(table, stride, width, lens, new, B, P, free, cap, count, lo, co, cu, slots, pos,
+                                     most, info, None)
+
+    def release(table=p, stride=8, width=8, lens=p, keep=p, B=2, P=16, free=p, cap=4, count=p, lo=p, co=p, info=p):
+        return lib.attn_pages_release(table, stride, width, lens, keep, B, P, free, cap, count, lo, co, info, None)
+
+    both = [dict(table=None), dict(stride=7), dict(width=-1), dict(width=1 << 28, stride=1 << 28), dict(lens=None),
+            dict(B=-1), dict(B=16385), dict(P=8), dict(P=48), dict(P=128), dict(free=None), dict(cap=-1),
+            dict(count=None), dict(lo=None), dict(co=None), dict(info=None)]
+    for bad in both + [dict(new=None), dict(cu=None), dict(slots=None), dict(pos=None), dict(most=-1)]:
+        assert assign(**bad) == ARG, bad
+    for bad in both + [dict(keep=None)]:
+        assert release(**bad) == ARG, bad
+
+
+def test_kv4_refusals(lib):  # noqa: F811
+    p = Buf().p
+    assert lib.attn_kv4_page_bytes(128, 16) == 2304 and lib.attn_kv4_page_bytes(1024, 64) == 73728
+    for d, s in ((96, 16), (0, 16), (1088, 16), (64, 8), (64, 48), (64, 0)):
+        assert lib.attn_kv4_page_bytes(d, s) == ARG
+
+    def append(k=p, kt=64, kh=64, v=p, vt=64, vh=64, slots=p, cache=p, pages=4, T=1, H=1, D=64, P=16):
+        return lib.attn_kv4_append(k, kt, kh, v, vt, vh, slots, cache, pages, T, H, D, P, None)
+
+    def read(cache=p, pages=4, slots=p, k=p, kh=64, kt=64, v=p, vh=64, vt=64, T=1, H=1, D=64, P=16):
+        return lib.attn_kv4_read(cache, pages, slots, k, kh, kt, v, vh, vt, T, H, D, P, None)
+
+    for call in (append, read):
+        for bad in (dict(k=None), dict(v=None), dict(slots=None), dict(cache=None), dict(pages=-1), dict(T=-1),
+                    dict(H=0), dict(H=65536), dict(D=96), dict(P=24), dict(kt=-8), dict(vh=-8), dict(pages=1 << 27)):
+            assert call(**bad) == ARG, (call, bad)
+        for bad in (dict(k=p + 2), dict(v=p + 8), dict(cache=p + 4), dict(slots=p + 1), dict(kh=4), dict(vt=12)):
+            assert call(**bad) == ALIGN, (call, bad)
+        assert call(T=0, k=None, v=None, slots=None) == 0
+
+    def fwd(q=p, qt=256, qh=64, cu=p, lens=p, table=p, stride=4, width=4, cache=p, pages=4, o=p, lse=p, B=1, T=1, Hq=4,
+            H=2, D=64, P=16, scale=0.125, causal=1):
+        return lib.attn_fwd_kv4(q, qt, qh, cu, lens, table, stride, width, cache, pages, o, lse, B, T, Hq, H, D, P,
+                                scale, causal, None)
+
+    for bad in (dict(q=None), dict(o=None), dict(lse=None), dict(cu=None), dict(lens=None), dict(table=None),
+                dict(cache=None), dict(stride=3), dict(width=-1), dict(pages=-1), dict(B=-1), dict(B=16385), dict(T=-1),
+                dict(Hq=0), dict(H=0), dict(Hq=5), dict(D=96), dict(D=320), dict(D=0), dict(P=8), dict(causal=2),
+                dict(scale=float("nan")), dict(scale=float("inf")), dict(qt=-8), dict(T=1 << 30, Hq=8, H=1)):
+        assert fwd(**bad) == ARG, bad
+    for bad in (dict(q=p + 2), dict(o=p + 8), dict(lse=p + 4), dict(cache=p + 8), dict(qh=4), dict(qt=12), dict(cu=p + 2),
+                dict(lens=p + 1), dict(table=p + 2)):
+        assert fwd(**bad) == ALIGN, bad
+    assert fwd(B=0, q=None) == 0 and fwd(T=0, q=None) == 0
+
+
+def test_binding_refuses_cpu_tensors_and_shapes(lib):  # noqa: F811
+    import exact_attention_attn_gb300 as A
+    bf, i32 = torch.bfloat16, torch.int32
+    q, pos = torch.zeros(1, 2, 3, 64, dtype=bf), torch.zeros(1, 1, 3, dtype=i32)
+    table = A.attn_rope_table(64, device="cpu")
+    with pytest.raises(ValueError, match="CUDA"):
+        A.attn_rope(q, None, pos, table)
+    with pytest.raises(TypeError, match="bfloat16"):
+        A.attn_rope(q.half(), None, pos, table)
+    with pytest.raises(ValueError, match="frequencies"):
+        A.attn_rope_table(64, [8, 8], device="cpu")
+    with pytest.raises(A.AttnError):
+        A.attn_rope_table(64, inv_freq=[float("nan")] * 32, device="cpu")
+    assert A.attn_rope_axes([3, 1, 2]) == [0, 0, 0, 1, 2, 2]
+    assert A.attn_rope_axes([3, 1, 2], interleave=True) == [0, 1, 2, 0, 2, 0]
+    with pytest.raises(A.AttnError):
+        A.attn_kv4_page_bytes(96, 16)
+    cache = A.attn_kv4_cache(2, 1, 64, 16, device="cpu")
+    assert cache.shape == (2, 1, 1152)
+    one = torch.zeros(1, dtype=i32)
+    for call in (lambda: A.attn_kv4_append(q[0], q[0], one, cache, 16), lambda: A.attn_kv4_read(one, cache, 16),
+                 lambda: A.attn_fwd_kv4(q[0], one, one, one[None], cache, 16),
+                 lambda: A.attn_pages_assign(one[None], one, one, one, one, 16, 4),
+                 lambda: A.attn_pages_release(one[None], one, one, one, one, 16)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
