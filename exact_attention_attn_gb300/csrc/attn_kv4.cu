@@ -58,10 +58,23 @@ namespace {
 
 using namespace ptx;
 
-constexpr int TK = 64;         // tokens per tile (a stage of the ring)
-constexpr int CW = 4;          // consumer warps, 16 tokens of a tile each
+#ifndef KV4_CW
+#define KV4_CW 4
+#endif
+#ifndef KV4_E
+#define KV4_E 4
+#endif
+#ifndef KV4_MIN
+#define KV4_MIN 1
+#endif
+#ifndef KV4_CTAS
+#define KV4_CTAS 0
+#endif
+constexpr int CW = KV4_CW;     // consumer warps, 16 tokens of a tile each
+constexpr int TK = CW * 16;    // tokens per tile (a stage of the ring)
 constexpr int CT = CW * 32;
 constexpr int THREADS = CT + 32;
+constexpr int START = KV4_E;   // an item's beginning and end cost about as much as this many tiles
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoRef = -1e37f;  // reference of a row that has seen no key
@@ -90,7 +103,7 @@ struct Kv4Params {
 struct Request {
   int t0, nq, len;   // first query token, query tokens, cached tokens
   int tiles, rt;     // tiles of 64 tokens (at least one), row tiles
-  __device__ __forceinline__ int64_t units(int H) const { return (int64_t)H * rt * tiles; }
+  __device__ __forceinline__ int64_t units(int H) const { return (int64_t)H * rt * (tiles + START); }
 };
 
 template <int R>
@@ -166,9 +179,9 @@ __device__ __forceinline__ void find_piece(const Kv4Params &p, Piece &pc) {
 // One (request, kv head, row tile) of a piece: tiles [tile0, tile0 + n).
 struct Item {
   Request q;
-  int h, rt, tile0, n;
+  int r, h, rt, tile0, n;
   bool whole;     // the piece holds all of the item
-  int64_t end;    // the item's last tile + 1, in the line
+  int64_t end;    // the item's last unit + 1, in the line
   // last visible key + 1 of row `row` (rows count query token x group head)
   __device__ __forceinline__ int limit(int row, const Kv4Params &p) const {
     const int i = row / p.group;
@@ -191,23 +204,30 @@ struct Walk {
   // Next item of the piece; false at its end.
   template <int R>
   __device__ __forceinline__ bool next(const Kv4Params &p, Item &it) {
-    if (at >= end) return false;
-    while (at >= base + q.units(p.H)) {  // also steps over requests without query tokens
-      base += q.units(p.H);
-      if (++r >= p.B) return false;
-      q = load_request<R>(p, r);
+    while (at < end) {
+      while (at >= base + q.units(p.H)) {  // also steps over requests without query tokens
+        base += q.units(p.H);
+        if (++r >= p.B) return false;
+        q = load_request<R>(p, r);
+      }
+      const int64_t local = at - base;
+      const int per = q.tiles + START;
+      const int64_t item = local / per;
+      const int off = (int)(local - item * per), n = (int)min((int64_t)(per - off), end - at);
+      const int tile0 = max(0, off - START), tile1 = max(0, off + n - START);
+      at += n;
+      if (tile0 == tile1) continue;  // no tile of the item itself: it begins in the next piece
+      it.q = q;
+      it.r = r;
+      it.tile0 = tile0;
+      it.h = (int)(item / q.rt);
+      it.rt = (int)(item - (int64_t)it.h * q.rt);
+      it.n = tile1 - tile0;
+      it.end = at - n - off + per;
+      it.whole = it.n == q.tiles;
+      return true;
     }
-    const int64_t local = at - base;
-    const int64_t item = local / q.tiles;
-    it.q = q;
-    it.tile0 = (int)(local - item * q.tiles);
-    it.h = (int)(item / q.rt);
-    it.rt = (int)(item - (int64_t)it.h * q.rt);
-    it.n = (int)min((int64_t)(q.tiles - it.tile0), end - at);
-    it.end = at - it.tile0 + q.tiles;
-    it.whole = it.n == q.tiles;
-    at += it.n;
-    return true;
+    return false;
   }
 };
 
@@ -283,16 +303,15 @@ __global__ void __launch_bounds__(THREADS) attn_kv4_kernel(const Kv4Params p) {
   Item it;
 
   if (warp == CW) {  // ---------------------------------------------------------------- producer
-    int n = 0;  // tiles issued
+    int n = 0, st = 0, ph = 1;  // tiles issued; stage, and the parity of its last release
     const int ppt = TK >> p.shift;  // pages of a tile
     bool ok = true;
     while (ok && walk.next<R>(p, it)) {
       const int last_row = min(it.q.nq * p.group, (it.rt + 1) * R) - 1;
       const int stop = min(it.tile0 + it.n, (it.limit(last_row, p) + TK - 1) / TK);
-      const int *row = p.table + (int64_t)walk.r * p.table_stride;
+      const int *row = p.table + (int64_t)it.r * p.table_stride;
       const int pages = (it.q.len + P - 1) >> p.shift;
       for (int tile = it.tile0; ok && tile < stop; ++tile, ++n) {
-        const int st = n % STAGES;
         const int pg = tile * ppt + lane;
         const bool have = lane < ppt && pg < pages;
         int id = have ? row[pg] : 0;
@@ -300,7 +319,7 @@ __global__ void __launch_bounds__(THREADS) attn_kv4_kernel(const Kv4Params p) {
           atomicCAS(p.status, 0, kStatusDevice);
           id = 0;
         }
-        if (n >= STAGES) ok = mbar_wait(&empty[st], ((n / STAGES) - 1) & 1, abort, p.wait_limit);
+        if (n >= STAGES) ok = mbar_wait(&empty[st], ph, abort, p.wait_limit);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
           atomicCAS(p.status, 0, kStatusTimeout);
@@ -313,6 +332,10 @@ __global__ void __launch_bounds__(THREADS) attn_kv4_kernel(const Kv4Params p) {
         if (have)
           bulk_load(smem + st * Sh::STAGE + lane * page_bytes, p.cache + ((int64_t)id * p.H + it.h) * page_bytes,
                     (uint32_t)page_bytes, &full[st]);
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1;
+        }
       }
     }
     // Every copy of this CTA lands before its shared memory is given back.
@@ -329,7 +352,8 @@ __global__ void __launch_bounds__(THREADS) attn_kv4_kernel(const Kv4Params p) {
   // index fall into different 32-byte quarters of the banks
   const int perm = (g >> 1) + ((g & 1) ? ((g >> 1) < 2 ? 6 : 2) : 0);
   const int vtok = ((t + 2) & 3) + 4;  // V token of k index 2t + 1 (that of 2t is t)
-  int n = 0;  // tiles consumed
+  int st = 0, ph = 0;  // stage of the next tile, and its parity
+  it.tile0 = -1;       // (a piece may hold no tile at all)
   while (walk.next<R>(p, it)) {
     const int rows = it.q.nq * p.group;
     const int row0 = it.rt * R;
@@ -425,9 +449,8 @@ __global__ void __launch_bounds__(THREADS) attn_kv4_kernel(const Kv4Params p) {
 #pragma unroll
     for (int j = 0; j < G; ++j) isig[j] = 0x1p100f;
 
-    for (int tile = it.tile0; tile < stop; ++tile, ++n) {
-      const int st = n % STAGES;
-      const bool got = mbar_wait(&full[st], (n / STAGES) & 1, abort, p.wait_limit);
+    for (int tile = it.tile0; tile < stop; ++tile) {
+      const bool got = mbar_wait(&full[st], ph, abort, p.wait_limit);
       if (!__all_sync(0xffffffffu, got)) {
         atomicCAS(p.status, 0, kStatusTimeout);
         *abort = 1;  // every role stops; the loops run out without waiting
@@ -441,7 +464,7 @@ __global__ void __launch_bounds__(THREADS) attn_kv4_kernel(const Kv4Params p) {
         const uint8_t *vc = kc + kv4_side_bytes(G, P), *vp = km + kv4_side_bytes(G, P);
         const int ta = tok0 + perm, tb = ta + 8;  // the lane's two tokens of S^T
         const bool edge = tok0 + 16 > full_to;
-        const bool in_a = ta < it.q.len, in_b = tb < it.q.len;
+const bool tail = tok0 + 16 > it.q.len;
 
         // S^T = K Q^T on the codes, joined over the groups with scales and minima
         float x[NT][4];
@@ -449,6 +472,8 @@ __global__ void __launch_bounds__(THREADS) attn_kv4_kernel(const Kv4Params p) {
         for (int j = 0; j < G; ++j) {
           const uint2 wa = *reinterpret_cast<const uint2 *>(kc + (j * P + perm) * kKv4RowBytes + t * 8);
           const uint2 wb = *reinterpret_cast<const uint2 *>(kc + (j * P + perm + 8) * kKv4RowBytes + t * 8);
+          const uint32_t pa = *reinterpret_cast<const uint32_t *>(km + (j * P + perm) * kKv4PairBytes);
+          const uint32_t pb = *reinterpret_cast<const uint32_t *>(km + (j * P + perm + 8) * kKv4PairBytes);
           float s[NT][4];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
@@ -465,72 +490,83 @@ __global__ void __launch_bounds__(THREADS) attn_kv4_kernel(const Kv4Params p) {
               xb >>= 8;
             }
           }
-          const uint32_t pa = *reinterpret_cast<const uint32_t *>(km + (j * P + perm) * kKv4PairBytes);
-          const uint32_t pb = *reinterpret_cast<const uint32_t *>(km + (j * P + perm + 8) * kKv4PairBytes);
           const float sa = __uint_as_float(pa << 16), ma = __uint_as_float(pa & 0xffff0000u);
           const float sb = __uint_as_float(pb << 16), mb = __uint_as_float(pb & 0xffff0000u);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const float za = fmaf(sa, s[nt][c], ma * qsum[nt][j][c]), zb = fmaf(sb, s[nt][2 + c], mb * qsum[nt][j][c]);
-              x[nt][c] = j ? x[nt][c] + za : za;
-              x[nt][2 + c] = j ? x[nt][2 + c] + zb : zb;
+              x[nt][c] = fmaf(sa, s[nt][c], j ? fmaf(ma, qsum[nt][j][c], x[nt][c]) : ma * qsum[nt][j][c]);
+              x[nt][2 + c] = fmaf(sb, s[nt][2 + c], j ? fmaf(mb, qsum[nt][j][c], x[nt][2 + c]) : mb * qsum[nt][j][c]);
             }
         }
-        // y in log2 units; hidden tokens -inf (selected, so that nothing they hold is used)
-        float y[NT][4];
+        // V's scales (over the warp's power of two) and minima of the lane's two tokens
+        float ua[G], ub[G], ma[G], mb[G];
+        float big_v = 0.f;
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          uint32_t pa = *reinterpret_cast<const uint32_t *>(vp + (j * P + perm) * kKv4PairBytes);
+          uint32_t pb = *reinterpret_cast<const uint32_t *>(vp + (j * P + perm + 8) * kKv4PairBytes);
+          if (tail) {  // nothing past the request's end is used, whatever it is
+            pa = ta < it.q.len ? pa : 0u;
+            pb = tb < it.q.len ? pb : 0u;
+          }
+          ua[j] = __uint_as_float(pa << 16) * isig[j];
+          ub[j] = __uint_as_float(pb << 16) * isig[j];
+          ma[j] = __uint_as_float(pa & 0xffff0000u);
+          mb[j] = __uint_as_float(pb & 0xffff0000u);
+          big_v = max3f(big_v, ua[j], ub[j]);
+        }
+        // e = y - ref in log2 units; hidden tokens -inf (selected, so that nothing they hold is used)
+        float e[NT][4];
         float top = -INFINITY;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float ya = x[nt][c] * fac[nt][c], yb = x[nt][2 + c] * fac[nt][c];
+            e[nt][c] = fmaf(x[nt][c], fac[nt][c], -ref[nt][c]);
+            e[nt][2 + c] = fmaf(x[nt][2 + c], fac[nt][c], -ref[nt][c]);
             if (edge) {
-              if (ta >= lim[nt][c]) ya = -INFINITY;
-              if (tb >= lim[nt][c]) yb = -INFINITY;
+              if (ta >= lim[nt][c]) e[nt][c] = -INFINITY;
+              if (tb >= lim[nt][c]) e[nt][2 + c] = -INFINITY;
             }
-            y[nt][c] = ya;
-            y[nt][2 + c] = yb;
-            top = max3f(top, ya - ref[nt][c], yb - ref[nt][c]);
+            top = max3f(top, e[nt][c], e[nt][2 + c]);
           }
-        // V's scales and minima of the lane's two tokens (none past the request's end)
-        float sa[G], sb[G], ma[G], mb[G];
-        bool over = top > 15.f;
-#pragma unroll
-        for (int j = 0; j < G; ++j) {
-          const uint32_t pa = in_a ? *reinterpret_cast<const uint32_t *>(vp + (j * P + perm) * kKv4PairBytes) : 0u;
-          const uint32_t pb = in_b ? *reinterpret_cast<const uint32_t *>(vp + (j * P + perm + 8) * kKv4PairBytes) : 0u;
-          sa[j] = __uint_as_float(pa << 16);
-          ma[j] = __uint_as_float(pa & 0xffff0000u);
-          sb[j] = __uint_as_float(pb << 16);
-          mb[j] = __uint_as_float(pb & 0xffff0000u);
-          over = over || fmaxf(sa[j], sb[j]) * isig[j] > 1.9f;
-        }
-        if (__any_sync(0xffffffffu, over)) {  // move the references up
+        if (__any_sync(0xffffffffu, top > 15.f || big_v > 1.9f)) {  // move the references up
           float fs[G];
 #pragma unroll
           for (int j = 0; j < G; ++j) {
-            float big = fmaxf(sa[j] < INFINITY ? sa[j] : 0.f, sb[j] < INFINITY ? sb[j] : 0.f);
+            // from the scales themselves: over the old power of two they may have overflowed
+            const uint32_t pa = *reinterpret_cast<const uint32_t *>(vp + (j * P + perm) * kKv4PairBytes);
+            const uint32_t pb = *reinterpret_cast<const uint32_t *>(vp + (j * P + perm + 8) * kKv4PairBytes);
+            const float sa = ta < it.q.len ? __uint_as_float(pa << 16) : 0.f;
+            const float sb = tb < it.q.len ? __uint_as_float(pb << 16) : 0.f;
+            float big = fmaxf(sa < INFINITY ? sa : 0.f, sb < INFINITY ? sb : 0.f);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
             fs[j] = 1.f;
-            if (big * isig[j] > 1.f) {  // big * 2^e in [0.5, 1)
-              const float now = pow2(min(126, max(-126, -1 - exp_of(fmaxf(big, 0x1p-120f)))));
+            if (big * isig[j] > 1.f) {  // the largest scale becomes [0.5, 1)
+              const float now = pow2(max(-126, -1 - exp_of(big)));
               fs[j] = now / isig[j];
               isig[j] = now;
+              ua[j] = sa * now;
+              ub[j] = sb * now;
             }
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float m = fmaxf(y[nt][c], y[nt][2 + c]);
+              const float ya = e[nt][c] == -INFINITY ? -INFINITY : x[nt][c] * fac[nt][c];
+              const float yb = e[nt][2 + c] == -INFINITY ? -INFINITY : x[nt][2 + c] * fac[nt][c];
+              float m = fmaxf(ya, yb);
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
               const float now = fmaxf(ref[nt][c], m - 10.f);
               const float f = ex2_approx(ref[nt][c] - now);
               ref[nt][c] = now;
+              e[nt][c] = ya - now;
+              e[nt][2 + c] = yb - now;
               l[nt][c] *= f;
 #pragma unroll
               for (int j = 0; j < G; ++j) {
@@ -548,26 +584,29 @@ __global__ void __launch_bounds__(THREADS) attn_kv4_kernel(const Kv4Params p) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            pr[nt][c] = ex2_approx(y[nt][c] - ref[nt][c]);
-            pr[nt][2 + c] = ex2_approx(y[nt][2 + c] - ref[nt][c]);
+            pr[nt][c] = ex2_approx(e[nt][c]);
+            pr[nt][2 + c] = ex2_approx(e[nt][2 + c]);
             l[nt][c] += pr[nt][c] + pr[nt][2 + c];
           }
         // O^T += V^T P^T
 #pragma unroll
         for (int j = 0; j < G; ++j) {
-          const float ua = sa[j] * isig[j], ub = sb[j] * isig[j];
           uint32_t b0[NT], b1[NT];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float w[4] = {pr[nt][0] * ua, pr[nt][1] * ua, pr[nt][2] * ub, pr[nt][3] * ub};
-            float e[4] = {pr[nt][0] * ma[j], pr[nt][1] * ma[j], pr[nt][2] * mb[j], pr[nt][3] * mb[j]};
-            if (edge) {  // a hidden token's scale may be anything
+            float w[4] = {pr[nt][0] * ua[j], pr[nt][1] * ua[j], pr[nt][2] * ub[j], pr[nt][3] * ub[j]};
+            if (!edge) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                if (y[nt][c] == -INFINITY) w[c] = e[c] = 0.f;
+              for (int c = 0; c < 2; ++c) vm[nt][j][c] = fmaf(pr[nt][2 + c], mb[j], fmaf(pr[nt][c], ma[j], vm[nt][j][c]));
+            } else {  // a hidden token's scale and minimum may be anything
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const bool no_a = e[nt][c] == -INFINITY, no_b = e[nt][2 + c] == -INFINITY;
+                if (no_a) w[c] = 0.f;
+                if (no_b) w[2 + c] = 0.f;
+                vm[nt][j][c] = fmaf(pr[nt][2 + c], no_b ? 0.f : mb[j], fmaf(pr[nt][c], no_a ? 0.f : ma[j], vm[nt][j][c]));
+              }
             }
-            vm[nt][j][0] += e[0] + e[2];
-            vm[nt][j][1] += e[1] + e[3];
             b0[nt] = transpose8x8(half2_bits(w[0], w[1]));
             b1[nt] = transpose8x8(half2_bits(w[2], w[3]));
           }
@@ -591,6 +630,10 @@ __global__ void __launch_bounds__(THREADS) attn_kv4_kernel(const Kv4Params p) {
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
+      if (++st == STAGES) {
+        st = 0;
+        ph ^= 1;
+      }
     }
 
     // ---- the item's end: sum over the lanes, then merge the warps
@@ -670,7 +713,7 @@ __global__ void __launch_bounds__(THREADS) attn_kv4_kernel(const Kv4Params p) {
   if (tid == 0) {
     int4 d = make_int4(0, 0, 0, 0);
     int last = 0;
-    if (pc.begin < pc.end && it.tile0 == 0 && !it.whole) {
+    if (it.tile0 == 0 && !it.whole) {
       d = make_int4(it.q.t0, it.h, it.rt * R, min(it.q.nq * p.group - it.rt * R, R));
       last = (int)((it.end - 1) / pc.chunk);  // the CTA that ends it
     }
@@ -792,9 +835,9 @@ int launch_kv4(Kv4Params &p, int device, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return record_cuda_error(e);
   // no more CTAs than there can be tiles
   const int64_t rows = (int64_t)p.T * p.group, row_tiles = rows / R + p.B;
-  const int64_t tiles = (((int64_t)p.max_pages << p.shift) + TK - 1) / TK;
+  const int64_t tiles = (((int64_t)p.max_pages << p.shift) + TK - 1) / TK + START;
   const int64_t most = row_tiles * p.H * (tiles < 1 ? 1 : tiles);
-  int grid = sms * per_sm;
+  int grid = sms * (KV4_CTAS ? KV4_CTAS : per_sm);
   if (grid > kMaxGrid) grid = kMaxGrid;
   if (grid > most) grid = (int)most;
   const size_t o_bytes = (size_t)grid * 2 * R * D * 4, ml_bytes = (size_t)grid * 2 * R * 8;
@@ -865,7 +908,7 @@ int attn_fwd_kv4(const void *q, long long q_stride_t, long long q_stride_h, cons
   p.max_pages = num_pages > 0 ? max_pages : 0;  // without pages no request holds a token
   p.B = B; p.T = T; p.H = Hkv; p.group = Hq / Hkv; p.shift = shift; p.causal = causal;
   p.scale_log2 = scale * kLog2e;
-  p.chunk_min = 1;
+  p.chunk_min = KV4_MIN;
   p.wait_limit = wait_limit_ns();
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // 16 rows a tile where the requests have more than 8 on average: K and V
