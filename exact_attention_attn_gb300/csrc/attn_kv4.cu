@@ -20,9 +20,10 @@
 // rows (query token x head of the kv head's group) are the 8 columns, so that
 // a decode step's 4 or 8 rows leave nothing or half of the tile unused:
 // S^T[token, row] = K Q^T and O^T[dim, row] = V^T P^T.  P^T is S^T's
-// accumulator transposed through movmatrix.  The order of the dims inside the
-// first product and of the tokens inside the second is free, and is chosen so
-// that every operand register comes from an aligned word of the page.
+// accumulator transposed through movmatrix.  ldmatrix hands every lane the
+// word of K's row that it multiplies, and, transposed as 16-bit elements (four
+// codes of one token), V's words with two tokens side by side, which is how
+// the second product wants them.  The order of the dims in a product is free.
 //
 // Softmax.  p = 2^(y - ref), ref a per-row reference 10 above which the warp
 // rescales only when some y exceeds ref + 15; P s' is rounded to half
@@ -31,16 +32,23 @@
 // largest scale, so that its products keep 11 bits down to 2^-24 of the
 // largest.  l and the sums of p m' are in float32.
 //
-// Work split.  The tiles of 64 tokens of all (request, kv head, row tile)
-// items form one line, cut into equal pieces, one per resident CTA: lengths
-// are read on the device, and no CTA is longer than another by more than a
-// tile.  An item cut by a piece's border leaves partial (ref, l, O) in a
-// workspace, at most two per CTA, which a second kernel -- launched early, its
-// wait overlapping the first's end -- merges in the order of the tokens.
+// Work split.  The tiles of 32 tokens of all (request, kv head, row tile)
+// items form one line, cut into equal pieces, one per resident warp: lengths
+// are read on the device, and no warp has more than another but for a tile.
+// An item's beginning and end cost a warp about as much as START tiles, so
+// each item is START units longer than its tiles in that line.  A warp works
+// alone -- it copies its own tiles, keeps its own softmax and writes its own
+// result -- so that the latencies of sixteen items overlap on an SM and short
+// requests cost no barrier.  An item cut by a piece's border leaves partial
+// (ref, l, O) in a workspace, at most two per warp, which a second kernel --
+// launched early, its wait overlapping the first's end -- merges in the order
+// of the tokens.
 //
-// Memory.  A producer warp copies each tile's pages (one contiguous bulk copy
-// per page: 36 bytes x D/32 per token) into a ring of stages; four consumer
-// warps take 16 tokens each.  Bound: HBM for up to 8 rows per kv head.
+// Memory.  Each warp owns a ring of stages of one tile; one bulk copy per page
+// (or, where a page is longer than a tile, per run of rows and pairs in it)
+// fills a stage, and the next tile is asked for as soon as a stage has been
+// read.  Bound: HBM and the issue of instructions, about evenly, for up to 8
+// rows per kv head.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -58,23 +66,20 @@ namespace {
 
 using namespace ptx;
 
-#ifndef KV4_CW
-#define KV4_CW 4
-#endif
 #ifndef KV4_E
-#define KV4_E 4
+#define KV4_E 3
+#endif
+#ifndef KV4_PARTS
+#define KV4_PARTS 64
 #endif
 #ifndef KV4_MIN
-#define KV4_MIN 1
+#define KV4_MIN 2
 #endif
-#ifndef KV4_CTAS
-#define KV4_CTAS 0
+#ifndef KV4_W2
+#define KV4_W2 12
 #endif
-constexpr int CW = KV4_CW;     // consumer warps, 16 tokens of a tile each
-constexpr int TK = CW * 16;    // tokens per tile (a stage of the ring)
-constexpr int CT = CW * 32;
-constexpr int THREADS = CT + 32;
-constexpr int START = KV4_E;   // an item's beginning and end cost about as much as this many tiles
+constexpr int kMostParts = KV4_PARTS;    // CTAs that one item is cut into, at most
+constexpr int kLeastUnits = KV4_MIN;     // units of a piece, at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoRef = -1e37f;  // reference of a row that has seen no key
@@ -90,23 +95,54 @@ struct Kv4Params {
   const uint8_t *cache;
   int num_pages, max_pages, B, T, H, group, shift, causal;
   float scale_log2;  // scale * log2 e
-  int chunk_min;     // least tiles of a CTA
-  float *ws_o;       // partial O of cut items: [grid][2][R][D]
-  float2 *ws_ml;     // their reference and l: [grid][2][R]
-  int4 *ws_cut;      // [grid][2]: the item that each CTA leaves unfinished
+  int pieces;        // warps of the grid
+  float *ws_o;       // partial O of cut items: [pieces][2][R][D]
+  float2 *ws_ml;     // their reference and l: [pieces][2][R]
+  int4 *ws_cut;      // [pieces][2]: the item that each piece leaves unfinished
   int *status;
-  uint64_t wait_limit;
+};
+
+// A variant: G groups of 64 dims, R query rows a tile, pages of P tokens.
+template <int G_, int R_, int P_>
+struct Shape {
+  static constexpr int G = G_, R = R_, P = P_;
+  static constexpr int D = G * kKv4Group;
+  static constexpr int NT = R / 8;                     // n8 tiles of rows
+  // tokens per tile (a stage of a warp's ring): whole pages, two of 16 tokens
+  static constexpr int TK = P > 32 ? P : 32;
+  static constexpr int PAGES = TK / P;
+  static constexpr int PAGE_BYTES = kv4_page_bytes(G, P);
+  static constexpr int STAGE = PAGES * PAGE_BYTES;
+  // Warps of a CTA (one CTA per SM), as the registers allow: 128 a thread for
+  // 64 dims, 168 for 128 dims or 16 rows of 64, 255 for more.
+  static constexpr int WARPS = G == 1 ? (R == 8 ? 16 : 12) : G == 2 && R == 8 ? KV4_W2 : G == 4 && P == 64 ? 6 : 8;
+  static constexpr int THREADS = WARPS * 32;
+  // as many stages as the SM's shared memory holds, 8 at most
+  static constexpr int FIT = 221184 / (WARPS * STAGE);
+  static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+  static constexpr int SMEM = WARPS * STAGES * STAGE;
+  // An item's beginning and end cost a warp about as much as this many tiles.
+  static constexpr int START = TK == 32 ? KV4_E : (KV4_E + 1) / 2;
+  // offset of group j's K rows and pairs of a stage's 16 tokens number i
+  static constexpr __host__ __device__ int code_row(int i, int j) {
+    return P == 16 ? i * PAGE_BYTES + j * P * kKv4RowBytes : (j * P + i * 16) * kKv4RowBytes;
+  }
+  static constexpr __host__ __device__ int pair_row(int i, int j) {
+    return P == 16 ? i * PAGE_BYTES + j * P * kKv4PairBytes : (j * P + i * 16) * kKv4PairBytes;
+  }
+  static_assert(STAGES >= 2, "a warp reads one stage while another fills");
+  static_assert(STAGES * STAGE >= R * D * 4, "a warp's part of a shared item fits its ring");
 };
 
 // What a request's tiles look like, from the device arrays, with whatever
 // they hold brought into range (reported once through the status word).
 struct Request {
   int t0, nq, len;   // first query token, query tokens, cached tokens
-  int tiles, rt;     // tiles of 64 tokens (at least one), row tiles
-  __device__ __forceinline__ int64_t units(int H) const { return (int64_t)H * rt * (tiles + START); }
+  int tiles, rt;     // tiles of tokens (at least one), row tiles
+  __device__ __forceinline__ int64_t units(int H, int start) const { return (int64_t)H * rt * (tiles + start); }
 };
 
-template <int R>
+template <typename S>
 __device__ __forceinline__ Request load_request(const Kv4Params &p, int r) {
   Request q;
   const int a = p.cu[r], b = p.cu[r + 1], l = p.lens[r];
@@ -116,64 +152,103 @@ __device__ __forceinline__ Request load_request(const Kv4Params &p, int r) {
   q.nq = t1 - q.t0;
   q.len = min(max(l, 0), room);
   if (q.t0 != a || t1 != b || q.len != l) atomicCAS(p.status, 0, kStatusDevice);
-  q.tiles = max(1, (q.len + TK - 1) / TK);
-  q.rt = (int)(((int64_t)q.nq * p.group + R - 1) / R);
+  q.tiles = max(1, (q.len + S::TK - 1) / S::TK);
+  q.rt = (int)(((int64_t)q.nq * p.group + S::R - 1) / S::R);
   return q;
 }
 
-// Position of a CTA's piece in the line of tiles.
+// A warp's piece of the line of units, and the item that holds the first unit
+// of its CTA's pieces.
 struct Piece {
   int64_t begin, end, chunk, total;
-  int r;            // request that holds tile `begin`
-  int64_t base;     // its first tile
+  int r;            // request that holds unit `begin`
+  int64_t base;     // its first unit
+  int64_t cta_begin, cta_end, item_begin, item_end;
+  int warps;        // pieces of a CTA
+  // one item covers the CTA, and more than one warp has a part of it
+  __device__ __forceinline__ bool shared() const { return item_end >= cta_end && cta_begin + chunk < cta_end; }
+  // ... and all of the item's tiles are in this CTA
+  __device__ __forceinline__ bool complete(int start) const { return item_begin + start >= cta_begin && item_end == cta_end; }
 };
 
-// All threads: total tiles, this CTA's piece, and the request it begins in.
-template <int R>
+// All threads of the CTA: each warp's piece, and the request it begins in.
+template <typename S>
 __device__ __forceinline__ void find_piece(const Kv4Params &p, Piece &pc) {
-  __shared__ int64_t wsum[THREADS / 32];
-  __shared__ int64_t found_base;
-  __shared__ int found_r;
+  __shared__ int64_t wsum[S::WARPS], found_base[S::WARPS], item[2];
+  __shared__ int wmax[S::WARPS], found_r[S::WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.B + THREADS - 1) / THREADS;  // consecutive requests of a thread
+  const int per = (p.B + S::THREADS - 1) / S::THREADS;  // consecutive requests of a thread
   const int r0 = min(tid * per, p.B), r1 = min(r0 + per, p.B);
   int64_t mine = 0;
-  for (int r = r0; r < r1; ++r) mine += load_request<R>(p, r).units(p.H);
+  int longest = 0;
+  for (int r = r0; r < r1; ++r) {
+    const Request q = load_request<S>(p, r);
+    mine += q.units(p.H, S::START);
+    longest = max(longest, q.tiles);
+  }
   int64_t inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += u;
   }
-  if (lane == 31) wsum[warp] = inc;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) {
+    wsum[warp] = inc;
+    wmax[warp] = longest;
+  }
   __syncthreads();
   int64_t before = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
+  for (int w = 0; w < S::WARPS; ++w) {
     if (w < warp) before += wsum[w];
     total += wsum[w];
+    longest = max(longest, wmax[w]);
   }
-  int64_t chunk = (total + gridDim.x - 1) / gridDim.x;
-  if (chunk < p.chunk_min) chunk = p.chunk_min;
-  pc.chunk = chunk;
-  pc.total = total;
-  pc.begin = min((int64_t)blockIdx.x * chunk, total);
-  pc.end = min(pc.begin + chunk, total);
-  int64_t at = before + inc - mine;
-  if (pc.begin >= at && pc.begin < at + mine) {
-    for (int r = r0; r < r1; ++r) {
-      const int64_t n = load_request<R>(p, r).units(p.H);
-      if (pc.begin < at + n) {
-        found_r = r;
-        found_base = at;
-        break;
+  // equal pieces, but none so small that one item would be cut into more than
+  // kMostParts CTAs: their merging would cost more than the tiles
+  const int64_t chunk = max(max((total + p.pieces - 1) / p.pieces, (int64_t)kLeastUnits),
+                            (int64_t)((longest + kMostParts * S::WARPS - 1) / (kMostParts * S::WARPS)));
+  // where there are few pieces they are spread over the CTAs
+  const int64_t used = (total + chunk - 1) / chunk;
+  const int warps = (int)min((int64_t)S::WARPS, (used + gridDim.x - 1) / gridDim.x);
+  const int64_t at = before + inc - mine;
+  if (mine > 0) {
+#pragma unroll
+    for (int w = 0; w < S::WARPS; ++w) {
+      const int64_t begin = ((int64_t)blockIdx.x * warps + w) * chunk;
+      if (w >= warps || begin < at || begin >= at + mine) continue;
+      int64_t a = at;
+      for (int r = r0; r < r1; ++r) {
+        const Request q = load_request<S>(p, r);
+        const int64_t n = q.units(p.H, S::START);
+        if (begin < a + n) {
+          found_r[w] = r;
+          found_base[w] = a;
+          if (w == 0) {
+            const int64_t i = (begin - a) / (q.tiles + S::START);
+            item[0] = a + i * (q.tiles + S::START);
+            item[1] = item[0] + q.tiles + S::START;
+          }
+          break;
+        }
+        a += n;
       }
-      at += n;
     }
   }
   __syncthreads();
-  pc.r = pc.begin < total ? found_r : 0;
-  pc.base = pc.begin < total ? found_base : 0;
+  pc.chunk = chunk;
+  pc.total = total;
+  pc.warps = warps;
+  pc.cta_begin = min((int64_t)blockIdx.x * warps * chunk, total);
+  pc.cta_end = min(pc.cta_begin + warps * chunk, total);
+  pc.begin = min(pc.cta_begin + warp * chunk, pc.cta_end);
+  pc.end = min(pc.begin + chunk, pc.cta_end);
+  const bool any = pc.begin < pc.end;
+  pc.r = any ? found_r[warp] : 0;
+  pc.base = any ? found_base[warp] : 0;
+  pc.item_begin = pc.cta_begin < total ? item[0] : 0;
+  pc.item_end = pc.cta_begin < total ? item[1] : 0;
 }
 
 // One (request, kv head, row tile) of a piece: tiles [tile0, tile0 + n).
@@ -193,28 +268,28 @@ struct Walk {
   int64_t at, end, base;
   int r;
   Request q;
-  template <int R>
+  template <typename S>
   __device__ __forceinline__ void start(const Kv4Params &p, const Piece &pc) {
     at = pc.begin;
     end = pc.end;
     base = pc.base;
     r = pc.r;
-    if (at < end) q = load_request<R>(p, r);
+    if (at < end) q = load_request<S>(p, r);
   }
   // Next item of the piece; false at its end.
-  template <int R>
+  template <typename S>
   __device__ __forceinline__ bool next(const Kv4Params &p, Item &it) {
     while (at < end) {
-      while (at >= base + q.units(p.H)) {  // also steps over requests without query tokens
-        base += q.units(p.H);
+      while (at >= base + q.units(p.H, S::START)) {  // also steps over requests without query tokens
+        base += q.units(p.H, S::START);
         if (++r >= p.B) return false;
-        q = load_request<R>(p, r);
+        q = load_request<S>(p, r);
       }
       const int64_t local = at - base;
-      const int per = q.tiles + START;
+      const int per = q.tiles + S::START;
       const int64_t item = local / per;
       const int off = (int)(local - item * per), n = (int)min((int64_t)(per - off), end - at);
-      const int tile0 = max(0, off - START), tile1 = max(0, off + n - START);
+      const int tile0 = max(0, off - S::START), tile1 = max(0, off + n - S::START);
       at += n;
       if (tile0 == tile1) continue;  // no tile of the item itself: it begins in the next piece
       it.q = q;
@@ -231,6 +306,12 @@ struct Walk {
   }
 };
 
+// Output row (token x query head) of row q of an item whose first query token is t0.
+__device__ __forceinline__ int64_t out_row(const Kv4Params &p, int t0, int h, int q) {
+  const int i = q / p.group;
+  return (int64_t)(t0 + i) * (p.H * p.group) + h * p.group + (q - i * p.group);
+}
+
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm volatile(
@@ -238,6 +319,36 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four 8x8 matrices of 16-bit elements; lanes 8 i .. 8 i + 7 give the rows of
+// the i-th.  Register i of lane (g, t): row g, elements 2t and 2t + 1 (or,
+// transposed, column g, rows 2t and 2t + 1).
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Waits until all but the warp's last N groups of copies have landed (each lane its own; then __syncwarp).
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t u;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(addr) : "memory");
+  return u;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
@@ -262,106 +373,110 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // Exponent e of x = f * 2^e, f in [1, 2), for a positive normal x.
 __device__ __forceinline__ int exp_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
 
-template <int G, int R>
-struct Kv4Shape {
-  static constexpr int D = G * kKv4Group;
-  static constexpr int NT = R / 8;                       // n8 tiles of rows
-  static constexpr int STAGE = TK * G * 2 * (kKv4RowBytes + kKv4PairBytes);
-  static constexpr int STAGES = G <= 2 ? 4 : 3;
-  static constexpr int MERGE_PITCH = D + 4;              // floats per row of the warps' merge buffer
-  static constexpr int MERGE = CW * R * MERGE_PITCH * 4;
-  static constexpr int SMEM = STAGES * STAGE + MERGE + 2 * CW * R * 4 + 2 * STAGES * 8 + 16;
-};
 
-template <int G, int R>
-__global__ void __launch_bounds__(THREADS) attn_kv4_kernel(const Kv4Params p) {
-  using Sh = Kv4Shape<G, R>;
-  constexpr int NT = Sh::NT, D = Sh::D, STAGES = Sh::STAGES;
+// The lane's part of the copy of tile `tile` of an item into the stage at
+// `dst`: 16 bytes of every 512.  The pages' ids are in the lanes (lane i: page
+// first + i; page 0 where the request has no further page, whose rows are
+// never used).
+template <typename S>
+__device__ __forceinline__ void copy_tile(const uint8_t *head, uint32_t page_row, int tile, int ids, int first,
+                                          uint32_t dst, int lane) {
+  constexpr int CHUNKS = S::STAGE / 16, PAGE = S::PAGE_BYTES / 16;  // of 16 bytes
+  const int at = tile * S::PAGES - first;
+  const uint32_t id0 = __shfl_sync(0xffffffffu, ids, at);
+  const uint8_t *src0 = head + (uint64_t)id0 * page_row + lane * 16, *src1 = src0;
+  if (S::PAGES == 2) {
+    const uint32_t id1 = __shfl_sync(0xffffffffu, ids, at + 1);
+    src1 = head + (uint64_t)id1 * page_row + lane * 16 - S::PAGE_BYTES;
+  }
+  dst += lane * 16;
+#pragma unroll
+  for (int k = 0; k * 32 < CHUNKS; ++k) {
+    const uint8_t *src = k * 32 + 31 < PAGE || S::PAGES == 1 ? src0 : k * 32 >= PAGE ? src1 : k * 32 + lane < PAGE ? src0 : src1;
+    if (k * 32 + 31 < CHUNKS || k * 32 + lane < CHUNKS) cp_async16(dst + k * 512, src + k * 512);
+  }
+}
+
+// Ids of 32 pages from `first` on, one a lane (what is not a page of the
+// cache is reported and read as the first page).
+__device__ __forceinline__ int load_ids(const Kv4Params &p, int r, int first, int pages, int lane) {
+  int id = 0;
+  if (first + lane < pages) {
+    id = p.table[(int64_t)r * p.table_stride + first + lane];
+    if ((unsigned)id >= (unsigned)p.num_pages) {
+      atomicCAS(p.status, 0, kStatusDevice);
+      id = 0;
+    }
+  }
+  return id;
+}
+
+template <typename S>
+__global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params p) {
+  constexpr int G = S::G, R = S::R, P = S::P, NT = S::NT, D = S::D, TK = S::TK;
+  constexpr int STAGES = S::STAGES, WARPS = S::WARPS, THREADS = S::THREADS;
   extern __shared__ __align__(128) uint8_t smem[];
-  float *merge_o = reinterpret_cast<float *>(smem + STAGES * Sh::STAGE);     // [CW][R][MERGE_PITCH]
-  float *merge_ref = merge_o + CW * R * Sh::MERGE_PITCH;                     // [CW][R]
-  float *merge_l = merge_ref + CW * R;                                       // [CW][R]
-  uint64_t *full = reinterpret_cast<uint64_t *>(merge_l + CW * R);
-  uint64_t *empty = full + STAGES;
-  volatile int *abort = reinterpret_cast<volatile int *>(empty + STAGES);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], CW);
-    }
-    *abort = 0;
-    fence_mbar_init();
-  }
-  Piece pc;
-  find_piece<R>(p, pc);  // its barriers also publish the mbarriers
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int P = 1 << p.shift;
-  const int page_bytes = kv4_page_bytes(G, P);
-  Walk walk;
-  walk.start<R>(p, pc);
+  uint8_t *ring = smem + warp * STAGES * S::STAGE;
+  __shared__ float2 warp_ml[WARPS][R];
+  __shared__ int4 warp_held[WARPS];
+  // What the loop over the tiles does not need waits in shared memory, so that
+  // the loop keeps its operands in registers.
+  __shared__ Walk walks[WARPS];
+  __shared__ Piece pieces[WARPS];
+  bool more;
   Item it;
-
-  if (warp == CW) {  // ---------------------------------------------------------------- producer
-    int n = 0, st = 0, ph = 1;  // tiles issued; stage, and the parity of its last release
-    const int ppt = TK >> p.shift;  // pages of a tile
-    bool ok = true;
-    while (ok && walk.next<R>(p, it)) {
-      const int last_row = min(it.q.nq * p.group, (it.rt + 1) * R) - 1;
-      const int stop = min(it.tile0 + it.n, (it.limit(last_row, p) + TK - 1) / TK);
-      const int *row = p.table + (int64_t)it.r * p.table_stride;
-      const int pages = (it.q.len + P - 1) >> p.shift;
-      for (int tile = it.tile0; ok && tile < stop; ++tile, ++n) {
-        const int pg = tile * ppt + lane;
-        const bool have = lane < ppt && pg < pages;
-        int id = have ? row[pg] : 0;
-        if ((unsigned)id >= (unsigned)p.num_pages) {  // not a page: report it and read the first one instead
-          atomicCAS(p.status, 0, kStatusDevice);
-          id = 0;
-        }
-        if (n >= STAGES) ok = mbar_wait(&empty[st], ph, abort, p.wait_limit);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          atomicCAS(p.status, 0, kStatusTimeout);
-          *abort = 1;
-          break;
-        }
-        const int cnt = min(ppt, pages - tile * ppt);
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(cnt * page_bytes));
-        __syncwarp();
-        if (have)
-          bulk_load(smem + st * Sh::STAGE + lane * page_bytes, p.cache + ((int64_t)id * p.H + it.h) * page_bytes,
-                    (uint32_t)page_bytes, &full[st]);
-        if (++st == STAGES) {
-          st = 0;
-          ph ^= 1;
-        }
-      }
+  {
+    Piece pc;
+    find_piece<S>(p, pc);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    Walk walk;
+    walk.start<S>(p, pc);
+    more = walk.next<S>(p, it);
+    if (lane == 0) {
+      pieces[warp] = pc;
+      walks[warp] = walk;
     }
-    // Every copy of this CTA lands before its shared memory is given back.
-    // (The consumers have waited for all of them unless a wait ran out.)
-    if (*abort)
-      for (int i = max(0, n - STAGES); i < n; ++i) mbar_wait_drain(&full[i % STAGES], (i / STAGES) & 1, p.wait_limit);
-    return;
+    __syncwarp();
   }
-
-  // ------------------------------------------------------------------------------------ consumers
+  const int piece = blockIdx.x * WARPS + warp;
   const int g = lane >> 2, t = lane & 3;
-  // token of row m of the K operand: 0 6 1 7 2 4 3 5 (+ 8 for the upper rows),
-  // which makes both the K rows a half warp reads and the V rows of one k
-  // index fall into different 32-byte quarters of the banks
-  const int perm = (g >> 1) + ((g & 1) ? ((g >> 1) < 2 ? 6 : 2) : 0);
-  const int vtok = ((t + 2) & 3) + 4;  // V token of k index 2t + 1 (that of 2t is t)
-  int st = 0, ph = 0;  // stage of the next tile, and its parity
-  it.tile0 = -1;       // (a piece may hold no tile at all)
-  while (walk.next<R>(p, it)) {
+  // the lane's row of the ldmatrix loads: matrices (tokens 0-7, 8-15) x (bytes 0-15, 16-31)
+  const uint32_t row_off = ((lane & 7) + ((lane >> 3) & 1) * 8) * kKv4RowBytes + (lane >> 4) * 16;
+  const uint32_t ring_s = smem_u32(ring);
+  const uint32_t page_row = (uint32_t)p.H * (uint32_t)S::PAGE_BYTES;
+
+  int st = 0;  // stage of the next tile
+  int4 cut = make_int4(0, 0, 0, 0);  // the item left unfinished (no rows: none) ...
+  int cut_last = 0, cut_flags = 0;   // ... the piece that ends it, and whether its first and last CTA share it (1, 2)
+  int4 held = make_int4(0, 0, 0, 0);  // the last item this warp worked on (query token, head, first row, rows)
+  // what the item's copies need: its tiles [tile0, stop), pages, and their ids
+  int stop, pages, first, ids, ids_next, asked;
+  const uint8_t *head;  // the kv head's block of the first page
+  auto begin_copies = [&]() {
+    const int last_row = min(it.q.nq * p.group, (it.rt + 1) * R) - 1;
+    stop = min(it.tile0 + it.n, (it.limit(last_row, p) + TK - 1) / TK);
+    pages = (it.q.len + P - 1) / P;
+    first = it.tile0 * S::PAGES;
+    head = p.cache + (int64_t)it.h * S::PAGE_BYTES;
+    ids = load_ids(p, it.r, first, pages, lane);
+    ids_next = load_ids(p, it.r, first + 32, pages, lane);
+    asked = it.tile0;
+    int s = st;
+    for (int i = 0; i < STAGES; ++i) {  // one group a stage, whether it copies or not; 32 ids cover the first tiles
+      if (asked < stop) copy_tile<S>(head, page_row, asked++, ids, first, ring_s + s * S::STAGE, lane);
+      cp_async_commit();
+      if (++s == STAGES) s = 0;
+    }
+  };
+  if (more) begin_copies();
+
+  while (more) {
     const int rows = it.q.nq * p.group;
     const int row0 = it.rt * R;
-    const int last_row = min(rows, row0 + R) - 1;
-    const int stop = min(it.tile0 + it.n, (it.limit(last_row, p) + TK - 1) / TK);
     const int full_to = min(it.limit(row0, p), it.q.len);  // tokens before it are visible to every row
 
-    // Q: lane (g, t) holds row g's dims of the words 2t, 2t + 1 of each group,
+    // Q: lane (g, t) holds row g's dims of word t of each half of each group,
     // scaled by a power of two so that the row's largest value is in [2^14, 2^15)
     uint32_t qb[NT][G][4][2];
     float fac[NT][2], qsum[NT][G][2];  // per column pair (rows 2t, 2t + 1): scale of y, sums of the scaled q
@@ -374,11 +489,11 @@ __global__ void __launch_bounds__(THREADS) attn_kv4_kernel(const Kv4Params p) {
       if (row < rows) {
         const int i = row / p.group, hg = row - i * p.group;
         const __nv_bfloat16 *src =
-            p.q + (int64_t)(it.q.t0 + i) * p.qt + (int64_t)(it.h * p.group + hg) * p.qh + t * 16;
+            p.q + (int64_t)(it.q.t0 + i) * p.qt + (int64_t)(it.h * p.group + hg) * p.qh + t * 8;
 #pragma unroll
         for (int j = 0; j < G; ++j) {
           w[j][0] = *reinterpret_cast<const uint4 *>(src + j * kKv4Group);
-          w[j][1] = *reinterpret_cast<const uint4 *>(src + j * kKv4Group + 8);
+          w[j][1] = *reinterpret_cast<const uint4 *>(src + j * kKv4Group + 32);
         }
       }
       float big = 0.f;
@@ -450,36 +565,35 @@ __global__ void __launch_bounds__(THREADS) attn_kv4_kernel(const Kv4Params p) {
     for (int j = 0; j < G; ++j) isig[j] = 0x1p100f;
 
     for (int tile = it.tile0; tile < stop; ++tile) {
-      const bool got = mbar_wait(&full[st], ph, abort, p.wait_limit);
-      if (!__all_sync(0xffffffffu, got)) {
-        atomicCAS(p.status, 0, kStatusTimeout);
-        *abort = 1;  // every role stops; the loops run out without waiting
-        continue;
-      }
-      const int tok0 = tile * TK + warp * 16;
-      if (tok0 < it.q.len) {
-        const int in = warp * 16, pgi = in >> p.shift, off = in & (P - 1);
-        const uint8_t *kc = smem + st * Sh::STAGE + pgi * page_bytes + off * kKv4RowBytes;
-        const uint8_t *km = smem + st * Sh::STAGE + pgi * page_bytes + kv4_codes_bytes(G, P) + off * kKv4PairBytes;
-        const uint8_t *vc = kc + kv4_side_bytes(G, P), *vp = km + kv4_side_bytes(G, P);
-        const int ta = tok0 + perm, tb = ta + 8;  // the lane's two tokens of S^T
-        const bool edge = tok0 + 16 > full_to;
-const bool tail = tok0 + 16 > it.q.len;
+      cp_async_wait<STAGES - 1>();
+      __syncwarp();
+#pragma unroll 1
+      for (int u = 0; u < TK / 32; ++u) {
+      const int tok0 = tile * TK + u * 32;
+      if (u > 0 && tok0 >= it.q.len) break;
+      const bool edge = tok0 + 32 > full_to, tail = tok0 + 32 > it.q.len;
+      // the first K row of each 16 tokens; everything else is at a fixed distance
+      const uint32_t kc = ring_s + st * S::STAGE + u * (S::code_row(2, 0) - S::code_row(0, 0)) + row_off;
+      const uint32_t km = ring_s + st * S::STAGE + u * (S::pair_row(2, 0) - S::pair_row(0, 0)) + kv4_codes_bytes(G, P) +
+                          g * kKv4PairBytes;
+      // the lane's tokens of S^T: ta, ta + 8 of each 16
+      const int ta = tok0 + g;
 
-        // S^T = K Q^T on the codes, joined over the groups with scales and minima
-        float x[NT][4];
+      // S^T = K Q^T on the codes, joined over the groups with scales and minima
+      float x[2][NT][4];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
         for (int j = 0; j < G; ++j) {
-          const uint2 wa = *reinterpret_cast<const uint2 *>(kc + (j * P + perm) * kKv4RowBytes + t * 8);
-          const uint2 wb = *reinterpret_cast<const uint2 *>(kc + (j * P + perm + 8) * kKv4RowBytes + t * 8);
-          const uint32_t pa = *reinterpret_cast<const uint32_t *>(km + (j * P + perm) * kKv4PairBytes);
-          const uint32_t pb = *reinterpret_cast<const uint32_t *>(km + (j * P + perm + 8) * kKv4PairBytes);
+          uint32_t w[4];  // tokens g and g + 8 of the first 32 dims, then of the others
+          ldmatrix4(w, kc + S::code_row(hf, j));
+          const uint32_t pa = lds32(km + S::pair_row(hf, j)), pb = lds32(km + S::pair_row(hf, j) + 8 * kKv4PairBytes);
           float s[NT][4];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            uint32_t xa = k ? wa.y : wa.x, xb = k ? wb.y : wb.x;
+            uint32_t xa = w[2 * k], xb = w[2 * k + 1];
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
               const uint32_t a0 = xa & 0x000f000fu, a1 = xb & 0x000f000fu, a2 = xa & 0x00f000f0u, a3 = xb & 0x00f000f0u;
@@ -496,127 +610,140 @@ const bool tail = tok0 + 16 > it.q.len;
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              x[nt][c] = fmaf(sa, s[nt][c], j ? fmaf(ma, qsum[nt][j][c], x[nt][c]) : ma * qsum[nt][j][c]);
-              x[nt][2 + c] = fmaf(sb, s[nt][2 + c], j ? fmaf(mb, qsum[nt][j][c], x[nt][2 + c]) : mb * qsum[nt][j][c]);
+              float &xa = x[hf][nt][c], &xb = x[hf][nt][2 + c];
+              xa = fmaf(sa, s[nt][c], j ? fmaf(ma, qsum[nt][j][c], xa) : ma * qsum[nt][j][c]);
+              xb = fmaf(sb, s[nt][2 + c], j ? fmaf(mb, qsum[nt][j][c], xb) : mb * qsum[nt][j][c]);
             }
         }
-        // V's scales (over the warp's power of two) and minima of the lane's two tokens
-        float ua[G], ub[G], ma[G], mb[G];
-        float big_v = 0.f;
+      }
+      // V's scales and minima of the lane's tokens (of those past the request's end none, whatever they are)
+      uint32_t pv[2][G][2];
+      float big_v = 0.f;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
         for (int j = 0; j < G; ++j) {
-          uint32_t pa = *reinterpret_cast<const uint32_t *>(vp + (j * P + perm) * kKv4PairBytes);
-          uint32_t pb = *reinterpret_cast<const uint32_t *>(vp + (j * P + perm + 8) * kKv4PairBytes);
-          if (tail) {  // nothing past the request's end is used, whatever it is
-            pa = ta < it.q.len ? pa : 0u;
-            pb = tb < it.q.len ? pb : 0u;
+          const uint32_t vp = km + kv4_side_bytes(G, P) + S::pair_row(hf, j);
+          pv[hf][j][0] = lds32(vp);
+          pv[hf][j][1] = lds32(vp + 8 * kKv4PairBytes);
+          if (tail) {
+            if (ta + hf * 16 >= it.q.len) pv[hf][j][0] = 0u;
+            if (ta + hf * 16 + 8 >= it.q.len) pv[hf][j][1] = 0u;
           }
-          ua[j] = __uint_as_float(pa << 16) * isig[j];
-          ub[j] = __uint_as_float(pb << 16) * isig[j];
-          ma[j] = __uint_as_float(pa & 0xffff0000u);
-          mb[j] = __uint_as_float(pb & 0xffff0000u);
-          big_v = max3f(big_v, ua[j], ub[j]);
+          big_v = max3f(big_v, __uint_as_float(pv[hf][j][0] << 16) * isig[j], __uint_as_float(pv[hf][j][1] << 16) * isig[j]);
         }
-        // e = y - ref in log2 units; hidden tokens -inf (selected, so that nothing they hold is used)
-        float e[NT][4];
-        float top = -INFINITY;
+      // e = y - ref in log2 units; hidden tokens -inf (selected, so that nothing they hold is used)
+      float e[2][NT][4];
+      float top = -INFINITY;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            e[nt][c] = fmaf(x[nt][c], fac[nt][c], -ref[nt][c]);
-            e[nt][2 + c] = fmaf(x[nt][2 + c], fac[nt][c], -ref[nt][c]);
+            float &ea = e[hf][nt][c], &eb = e[hf][nt][2 + c];
+            ea = fmaf(x[hf][nt][c], fac[nt][c], -ref[nt][c]);
+            eb = fmaf(x[hf][nt][2 + c], fac[nt][c], -ref[nt][c]);
             if (edge) {
-              if (ta >= lim[nt][c]) e[nt][c] = -INFINITY;
-              if (tb >= lim[nt][c]) e[nt][2 + c] = -INFINITY;
+              if (ta + hf * 16 >= lim[nt][c]) ea = -INFINITY;
+              if (ta + hf * 16 + 8 >= lim[nt][c]) eb = -INFINITY;
             }
-            top = max3f(top, e[nt][c], e[nt][2 + c]);
+            top = max3f(top, ea, eb);
           }
-        if (__any_sync(0xffffffffu, top > 15.f || big_v > 1.9f)) {  // move the references up
-          float fs[G];
+      if (__any_sync(0xffffffffu, top > 15.f || big_v > 1.9f)) {  // move the references up
+        float fs[G];
 #pragma unroll
-          for (int j = 0; j < G; ++j) {
-            // from the scales themselves: over the old power of two they may have overflowed
-            const uint32_t pa = *reinterpret_cast<const uint32_t *>(vp + (j * P + perm) * kKv4PairBytes);
-            const uint32_t pb = *reinterpret_cast<const uint32_t *>(vp + (j * P + perm + 8) * kKv4PairBytes);
-            const float sa = ta < it.q.len ? __uint_as_float(pa << 16) : 0.f;
-            const float sb = tb < it.q.len ? __uint_as_float(pb << 16) : 0.f;
-            float big = fmaxf(sa < INFINITY ? sa : 0.f, sb < INFINITY ? sb : 0.f);
+        for (int j = 0; j < G; ++j) {
+          float big = 0.f;  // from the scales themselves: over the old power of two they may have overflowed
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-            fs[j] = 1.f;
-            if (big * isig[j] > 1.f) {  // the largest scale becomes [0.5, 1)
-              const float now = pow2(max(-126, -1 - exp_of(big)));
-              fs[j] = now / isig[j];
-              isig[j] = now;
-              ua[j] = sa * now;
-              ub[j] = sb * now;
-            }
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const float ya = e[nt][c] == -INFINITY ? -INFINITY : x[nt][c] * fac[nt][c];
-              const float yb = e[nt][2 + c] == -INFINITY ? -INFINITY : x[nt][2 + c] * fac[nt][c];
-              float m = fmaxf(ya, yb);
+              const float s = __uint_as_float(pv[hf][j][c] << 16);
+              big = fmaxf(big, s < INFINITY ? s : 0.f);
+            }
 #pragma unroll
-              for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-              const float now = fmaxf(ref[nt][c], m - 10.f);
-              const float f = ex2_approx(ref[nt][c] - now);
-              ref[nt][c] = now;
-              e[nt][c] = ya - now;
-              e[nt][2 + c] = yb - now;
-              l[nt][c] *= f;
+          for (int o = 4; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+          fs[j] = 1.f;
+          if (big * isig[j] > 1.f) {  // the largest scale becomes [0.5, 1)
+            const float now = pow2(max(-126, -1 - exp_of(big)));
+            fs[j] = now / isig[j];
+            isig[j] = now;
+          }
+        }
 #pragma unroll
-              for (int j = 0; j < G; ++j) {
-                vm[nt][j][c] *= f;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                  acc[nt][j][d][c] *= f * fs[j];
-                  acc[nt][j][d][2 + c] *= f * fs[j];
-                }
+          for (int c = 0; c < 2; ++c) {
+            float m = -INFINITY;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int u = c; u < 4; u += 2)
+                if (e[hf][nt][u] != -INFINITY) m = fmaxf(m, x[hf][nt][u] * fac[nt][c]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float now = fmaxf(ref[nt][c], m - 10.f);
+            const float f = ex2_approx(ref[nt][c] - now);
+            ref[nt][c] = now;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int u = c; u < 4; u += 2)
+                if (e[hf][nt][u] != -INFINITY) e[hf][nt][u] = fmaf(x[hf][nt][u], fac[nt][c], -now);
+            l[nt][c] *= f;
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+              vm[nt][j][c] *= f;
+#pragma unroll
+              for (int d = 0; d < 4; ++d) {
+                acc[nt][j][d][c] *= f * fs[j];
+                acc[nt][j][d][2 + c] *= f * fs[j];
               }
             }
-        }
+          }
+      }
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
         float pr[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            pr[nt][c] = ex2_approx(e[nt][c]);
-            pr[nt][2 + c] = ex2_approx(e[nt][2 + c]);
+            pr[nt][c] = ex2_approx(e[hf][nt][c]);
+            pr[nt][2 + c] = ex2_approx(e[hf][nt][2 + c]);
             l[nt][c] += pr[nt][c] + pr[nt][2 + c];
           }
         // O^T += V^T P^T
 #pragma unroll
         for (int j = 0; j < G; ++j) {
+          const uint32_t pa = pv[hf][j][0], pb = pv[hf][j][1];
+          const float ua = __uint_as_float(pa << 16) * isig[j], ub = __uint_as_float(pb << 16) * isig[j];
+          const float ma = __uint_as_float(pa & 0xffff0000u), mb = __uint_as_float(pb & 0xffff0000u);
           uint32_t b0[NT], b1[NT];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float w[4] = {pr[nt][0] * ua[j], pr[nt][1] * ua[j], pr[nt][2] * ub[j], pr[nt][3] * ub[j]};
+            float w[4] = {pr[nt][0] * ua, pr[nt][1] * ua, pr[nt][2] * ub, pr[nt][3] * ub};
             if (!edge) {
 #pragma unroll
-              for (int c = 0; c < 2; ++c) vm[nt][j][c] = fmaf(pr[nt][2 + c], mb[j], fmaf(pr[nt][c], ma[j], vm[nt][j][c]));
+              for (int c = 0; c < 2; ++c) vm[nt][j][c] = fmaf(pr[nt][2 + c], mb, fmaf(pr[nt][c], ma, vm[nt][j][c]));
             } else {  // a hidden token's scale and minimum may be anything
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const bool no_a = e[nt][c] == -INFINITY, no_b = e[nt][2 + c] == -INFINITY;
+                const bool no_a = e[hf][nt][c] == -INFINITY, no_b = e[hf][nt][2 + c] == -INFINITY;
                 if (no_a) w[c] = 0.f;
                 if (no_b) w[2 + c] = 0.f;
-                vm[nt][j][c] = fmaf(pr[nt][2 + c], no_b ? 0.f : mb[j], fmaf(pr[nt][c], no_a ? 0.f : ma[j], vm[nt][j][c]));
+                vm[nt][j][c] = fmaf(pr[nt][2 + c], no_b ? 0.f : mb, fmaf(pr[nt][c], no_a ? 0.f : ma, vm[nt][j][c]));
               }
             }
             b0[nt] = transpose8x8(half2_bits(w[0], w[1]));
             b1[nt] = transpose8x8(half2_bits(w[2], w[3]));
           }
-          const uint8_t *v0 = vc + (j * P + t) * kKv4RowBytes + g * 4, *v1 = vc + (j * P + vtok) * kKv4RowBytes + g * 4;
-          const uint32_t x0 = *reinterpret_cast<const uint32_t *>(v0), x1 = *reinterpret_cast<const uint32_t *>(v1);
-          const uint32_t x2 = *reinterpret_cast<const uint32_t *>(v0 + 8 * kKv4RowBytes);
-          const uint32_t x3 = *reinterpret_cast<const uint32_t *>(v1 + 8 * kKv4RowBytes);
+          uint32_t z[4];  // dims 4g .. 4g + 3 of tokens (2t, 2t + 1) and (8 + 2t, 9 + 2t), then those of the other 32 dims
+          ldmatrix4_trans(z, kc + kv4_side_bytes(G, P) + S::code_row(hf, j));
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {  // dims 0-3, then 4-7 of the lane's 8
-            uint32_t z0 = __byte_perm(x0, x1, k ? 0x7632 : 0x5410), z1 = __byte_perm(x2, x3, k ? 0x7632 : 0x5410);
+          for (int k = 0; k < 2; ++k) {
+            uint32_t z0 = z[2 * k], z1 = z[2 * k + 1];
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
               const uint32_t a0 = z0 & 0x000f000fu, a1 = z0 & 0x00f000f0u, a2 = z1 & 0x000f000fu, a3 = z1 & 0x00f000f0u;
@@ -628,15 +755,45 @@ const bool tail = tok0 + 16 > it.q.len;
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
-      if (++st == STAGES) {
-        st = 0;
-        ph ^= 1;
       }
+      __syncwarp();  // every lane has read the stage
+      if (asked < stop) {
+        if (asked * S::PAGES - first >= 32) {
+          first += 32;
+          ids = ids_next;
+          ids_next = load_ids(p, it.r, first + 32, pages, lane);
+        }
+        copy_tile<S>(head, page_row, asked++, ids, first, ring_s + st * S::STAGE, lane);
+      }
+      cp_async_commit();
+      if (++st == STAGES) st = 0;
     }
 
-    // ---- the item's end: sum over the lanes, then merge the warps
+    // ---- the item's end: the next item's first tiles are asked for, then the lanes are summed and the rows written
+    const Item done = it;
+    const Piece &pc = pieces[warp];
+    {
+      Walk walk = walks[warp];
+      more = walk.next<S>(p, it);
+      __syncwarp();
+      if (lane == 0) walks[warp] = walk;
+      __syncwarp();
+    }
+    const bool part_s = pc.shared();  // a part of the item that the whole CTA shares
+    const bool whole = done.whole && !part_s;
+    if (more) begin_copies();
+    if (done.tile0 == 0 && !whole && !(part_s && pc.complete(S::START))) {
+      cut = make_int4(done.q.t0, done.h, row0, min(rows - row0, R));
+      cut_last = (int)((done.end - 1) / pc.chunk);
+      const int64_t last_begin = (int64_t)(cut_last / pc.warps) * pc.warps * pc.chunk;
+      const int64_t last_end = min(last_begin + pc.warps * pc.chunk, pc.total);
+      cut_flags = (part_s ? 1 : 0) |
+                  (cut_last / pc.warps != (int)blockIdx.x && done.end >= last_end && last_begin + pc.chunk < last_end ? 2 : 0);
+    }
+    // a shared item's part goes to shared memory (this warp's ring, empty by now)
+    const int64_t part = ((int64_t)piece * 2 + (done.tile0 > 0 ? 0 : 1)) * R;
+    float *const part_o = part_s ? reinterpret_cast<float *>(ring) : p.ws_o + part * D;
+    float2 *const part_ml = part_s ? warp_ml[warp] : p.ws_ml + part;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -647,213 +804,279 @@ const bool tail = tok0 + 16 > it.q.len;
 #pragma unroll
           for (int j = 0; j < G; ++j) vm[nt][j][c] += __shfl_xor_sync(0xffffffffu, vm[nt][j][c], o);
         }
-        const int row = nt * 8 + 2 * t + c;
-        if (g == 0) {
-          merge_ref[warp * R + row] = ref[nt][c];
-          merge_l[warp * R + row] = l[nt][c];
-        }
-        float *dst = merge_o + (warp * R + row) * Sh::MERGE_PITCH + g * 8;
+        const int row = nt * 8 + 2 * t + c, q = row0 + row;
+        if (q >= rows) continue;
+        const bool none = saw_none(ref[nt][c], l[nt][c]);
+        const float inv = whole ? (none ? 0.f : 1.f / l[nt][c]) : 1.f;
+        const int64_t at = out_row(p, done.q.t0, done.h, q);
 #pragma unroll
         for (int j = 0; j < G; ++j) {
           const float sig = 0x1p24f / isig[j], m = vm[nt][j][c];
-          float4 lo, hi;
-          lo.x = fmaf(acc[nt][j][0][c], sig, m);
-          lo.y = fmaf(acc[nt][j][0][2 + c], sig * 0.0625f, m);
-          lo.z = fmaf(acc[nt][j][1][c], sig, m);
-          lo.w = fmaf(acc[nt][j][1][2 + c], sig * 0.0625f, m);
-          hi.x = fmaf(acc[nt][j][2][c], sig, m);
-          hi.y = fmaf(acc[nt][j][2][2 + c], sig * 0.0625f, m);
-          hi.z = fmaf(acc[nt][j][3][c], sig, m);
-          hi.w = fmaf(acc[nt][j][3][2 + c], sig * 0.0625f, m);
-          *reinterpret_cast<float4 *>(dst + j * kKv4Group) = lo;
-          *reinterpret_cast<float4 *>(dst + j * kKv4Group + 4) = hi;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float o[4];
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              o[2 * d] = fmaf(acc[nt][j][2 * k + d][c], sig, m) * inv;
+              o[2 * d + 1] = fmaf(acc[nt][j][2 * k + d][2 + c], sig * 0.0625f, m) * inv;
+            }
+            const int dim = j * kKv4Group + k * 32 + g * 4;
+            if (whole)
+              *reinterpret_cast<uint2 *>(p.o + at * D + dim) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+            else
+              *reinterpret_cast<float4 *>(part_o + row * D + dim) = make_float4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        if (g == 0) {
+          if (whole)
+            p.lse[at] = none ? -INFINITY : (ref[nt][c] + log2f(l[nt][c])) * kLn2;
+          else
+            part_ml[row] = make_float2(ref[nt][c], l[nt][c]);
         }
       }
-    asm volatile("bar.sync 1, %0;" ::"n"(CT) : "memory");
-    const int slot = it.tile0 > 0 ? 0 : 1;
-    const int64_t part = ((int64_t)blockIdx.x * 2 + slot) * R;
-    for (int i = tid; i < R * (D / 4); i += CT) {
-      const int row = i / (D / 4), d = (i % (D / 4)) * 4, q = row0 + row;
-      if (q >= rows) break;
-      float m = merge_ref[row];
+    held = make_int4(done.q.t0, done.h, row0, min(rows - row0, R));
+  }
+  const Piece &pc = pieces[warp];
+  if (pc.shared()) {
+    // The warps' parts of the one item, merged: to the output if that is all of it, else to the CTA's partial.
+    if (lane == 0) warp_held[warp] = held;
+    __syncthreads();
+    int4 d = warp_held[0];
 #pragma unroll
-      for (int w = 1; w < CW; ++w) m = fmaxf(m, merge_ref[w * R + row]);
+    for (int w = 1; w < WARPS; ++w)
+      if (d.w == 0) d = warp_held[w];  // (a warp may have had none of its tiles)
+    const bool all = pc.complete(S::START);
+    const int64_t part = (int64_t)blockIdx.x * WARPS * 2 * R;
+    for (int i = tid; i < d.w * (D / 4); i += THREADS) {
+      const int row = i / (D / 4), dim = (i % (D / 4)) * 4;
+      float m = kNoRef, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w)
+        if (warp_held[w].w) m = fmaxf(m, warp_ml[w][row].x);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < CW; ++w) {
-        const float f = ex2_approx(merge_ref[w * R + row] - m);
-        const float4 v = *reinterpret_cast<const float4 *>(merge_o + (w * R + row) * Sh::MERGE_PITCH + d);
-        if (saw_none(merge_ref[w * R + row], merge_l[w * R + row])) continue;
-        sum = fmaf(merge_l[w * R + row], f, sum);
-        o.x = fmaf(v.x, f, o.x);
-        o.y = fmaf(v.y, f, o.y);
-        o.z = fmaf(v.z, f, o.z);
-        o.w = fmaf(v.w, f, o.w);
+      for (int w = 0; w < WARPS; ++w) {
+        if (warp_held[w].w == 0) continue;
+        const float2 ml = warp_ml[w][row];
+        if (saw_none(ml.x, ml.y)) continue;
+        const float f = ex2_approx(ml.x - m);
+        const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + w * STAGES * S::STAGE) + row * D + dim);
+        l = fmaf(f, ml.y, l);
+        o.x = fmaf(f, v.x, o.x);
+        o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z);
+        o.w = fmaf(f, v.w, o.w);
       }
-      if (it.whole) {
-        const bool none = saw_none(m, sum);
-        const float inv = none ? 0.f : 1.f / sum;
-        const int64_t at = (int64_t)(it.q.t0 + q / p.group) * (p.H * p.group) + it.h * p.group + q % p.group;
-        const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), h1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-        uint2 u;
-        memcpy(&u.x, &h0, 4);
-        memcpy(&u.y, &h1, 4);
-        *reinterpret_cast<uint2 *>(p.o + at * D + d) = u;
-        if (d == 0) p.lse[at] = none ? -INFINITY : (m + log2f(sum)) * kLn2;
+      if (all) {
+        const bool none = saw_none(m, l);
+        const float inv = none ? 0.f : 1.f / l;
+        const int64_t at = out_row(p, d.x, d.y, d.z + row);
+        *reinterpret_cast<uint2 *>(p.o + at * D + dim) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (dim == 0) p.lse[at] = none ? -INFINITY : (m + log2f(l)) * kLn2;
       } else {
-        *reinterpret_cast<float4 *>(p.ws_o + (part + row) * D + d) = o;
-        if (d == 0) p.ws_ml[part + row] = make_float2(m, sum);
+        *reinterpret_cast<float4 *>(p.ws_o + (part + row) * D + dim) = o;
+        if (dim == 0) p.ws_ml[part + row] = make_float2(m, l);
       }
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(CT) : "memory");  // the merge buffer is free again
   }
-  // What the second kernel has to merge: the item that began here and goes on
-  // in later CTAs, or nothing (no rows).
-  if (tid == 0) {
-    int4 d = make_int4(0, 0, 0, 0);
-    int last = 0;
-    if (it.tile0 == 0 && !it.whole) {
-      d = make_int4(it.q.t0, it.h, it.rt * R, min(it.q.nq * p.group - it.rt * R, R));
-      last = (int)((it.end - 1) / pc.chunk);  // the CTA that ends it
-    }
-    p.ws_cut[blockIdx.x * 2] = d;
-    p.ws_cut[blockIdx.x * 2 + 1] = make_int4(last, 0, 0, 0);
+  if (lane == 0) {
+    p.ws_cut[piece * 2] = cut;
+    p.ws_cut[piece * 2 + 1] = make_int4(cut_last, cut_flags, pc.warps, 0);
   }
 }
 
-// Merges the partials of one row of the item that CTA blockIdx.x of the first
-// kernel began and left unfinished: that CTA's second partial and the first
-// partials of the CTAs after it, up to the one that ends the item.  With
-// M = max ref_i:  O = sum 2^(ref_i - M) O_i / sum 2^(ref_i - M) l_i.  The
-// weights go through shared memory first, so that every load of a partial is
-// independent; the partials are summed in a fixed order.
-constexpr int kMergeThreads = 256;
-constexpr int kMaxGrid = 2048;
+// Merges the items that the pieces of CTA blockIdx.x of the first kernel began
+// and left unfinished.  Their parts, in order: the beginning piece's second
+// partial and the first partials of the pieces after it in that CTA, one
+// partial for each CTA that shares the item, the first partials of the last
+// CTA's pieces.  With M = max ref_i:
+//     O = sum 2^(ref_i - M) O_i / sum 2^(ref_i - M) l_i.
+// The rows of all these items are the CTA's tasks; a warp sums every per-th
+// part of one of them with a running reference, several loads in flight, and
+// the warps of a row are joined through shared memory: a fixed order.
+constexpr int kMergeWarps = 16;
+constexpr int kMergeThreads = kMergeWarps * 32;
 
-template <int G>
-__global__ void __launch_bounds__(kMergeThreads) attn_kv4_merge_kernel(const Kv4Params p, int R) {
-  constexpr int D = G * kKv4Group, COLS = D / 4, NG = kMergeThreads / COLS;
-  __shared__ float weight[kMaxGrid];
-  __shared__ float red[kMergeThreads / 32];
-  __shared__ __align__(16) float part[NG][D];
+template <typename S>
+__global__ void __launch_bounds__(kMergeThreads) attn_kv4_merge_kernel(const Kv4Params p) {
+  constexpr int D = S::D, R = S::R, WARPS = S::WARPS, V = (D / 4 + 31) / 32;  // float4s of a lane
+  constexpr int U = V == 1 ? 8 : 4;                        // parts in flight
+  __shared__ __align__(16) float part[kMergeWarps][D];
+  __shared__ float2 part_ml[kMergeWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x * WARPS;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
-  const int4 d = p.ws_cut[2 * c];
-  if (row >= d.w) return;
-  const int n = p.ws_cut[2 * c + 1].x - c + 1;
-  auto index = [&](int i) { return ((int64_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * R + row; };
-  auto reduce = [&](float v, bool sum) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float u = __shfl_xor_sync(0xffffffffu, v, o);
-      v = sum ? v + u : fmaxf(v, u);
-    }
-    if ((tid & 31) == 0) red[tid >> 5] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int w = 1; w < kMergeThreads / 32; ++w) v = sum ? v + red[w] : fmaxf(v, red[w]);
-    __syncthreads();
-    return v;
-  };
-  float m = kNoRef;
-  for (int i = tid; i < n; i += kMergeThreads) m = fmaxf(m, p.ws_ml[index(i)].x);
-  m = reduce(m, false);
-  float l = 0.f;
-  for (int i = tid; i < n; i += kMergeThreads) {
-    const float2 ml = p.ws_ml[index(i)];
-    const float f = saw_none(ml.x, ml.y) ? 0.f : ex2_approx(ml.x - m);
-    weight[i] = f;
-    l = fmaf(f, ml.y, l);
+  // lane k: the item that piece k left unfinished, and its rows summed up to it
+  int4 cut = make_int4(0, 0, 0, 0), end = cut;
+  if (lane < WARPS) {
+    cut = p.ws_cut[2 * (c0 + lane)];
+    end = p.ws_cut[2 * (c0 + lane) + 1];
   }
-  l = reduce(l, true);
-  const int grp = tid / COLS, col = (tid % COLS) * 4;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (grp < NG) {
-#pragma unroll 4
-    for (int i = grp; i < n; i += NG) {
-      const float f = weight[i];
-      const float4 v = *reinterpret_cast<const float4 *>(p.ws_o + index(i) * D + col);
-      o.x = fmaf(f, v.x, o.x);
-      o.y = fmaf(f, v.y, o.y);
-      o.z = fmaf(f, v.z, o.z);
-      o.w = fmaf(f, v.w, o.w);
-    }
-    *reinterpret_cast<float4 *>(&part[grp][col]) = o;
-  }
-  __syncthreads();
-  const bool none = saw_none(m, l);
-  const float inv = none ? 0.f : 1.f / l;
-  const int q = d.z + row;
-  const int64_t at = (int64_t)(d.x + q / p.group) * (p.H * p.group) + d.y * p.group + q % p.group;
-  if (tid < COLS) {
+  int sum = cut.w;
 #pragma unroll
-    for (int w = 1; w < NG; ++w) {
-      const float4 v = *reinterpret_cast<const float4 *>(&part[w][col]);
-      o.x += v.x;
-      o.y += v.y;
-      o.z += v.z;
-      o.w += v.w;
-    }
-    const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), h1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-    uint2 u;
-    memcpy(&u.x, &h0, 4);
-    memcpy(&u.y, &h1, 4);
-    *reinterpret_cast<uint2 *>(p.o + at * D + col) = u;
+  for (int x = 1; x < 32; x <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, sum, x);
+    if (lane >= x) sum += u;
   }
-  if (tid == 0) p.lse[at] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+  const int tasks = __shfl_sync(0xffffffffu, sum, 31);
+  // warps of a task: the most that leaves every task some
+  const int per = tasks >= 9 ? 1 : tasks >= 5 ? 2 : tasks >= 3 ? 4 : tasks == 2 ? 8 : 16;
+  for (int task0 = 0; task0 < tasks; task0 += kMergeWarps / per) {
+    const int task = task0 + warp / per, sub = warp % per;
+    const bool mine = task < tasks;
+    const int k = __popc(__ballot_sync(0xffffffffu, sum <= task)) & 31;
+    const int4 d = make_int4(__shfl_sync(0xffffffffu, cut.x, k), __shfl_sync(0xffffffffu, cut.y, k),
+                             __shfl_sync(0xffffffffu, cut.z, k), __shfl_sync(0xffffffffu, cut.w, k));
+    const int3 e = make_int3(__shfl_sync(0xffffffffu, end.x, k), __shfl_sync(0xffffffffu, end.y, k),
+                             __shfl_sync(0xffffffffu, end.z, k));
+    const int row = task - (__shfl_sync(0xffffffffu, sum, k) - d.w);
+    float m = kNoRef, l = 0.f;
+    float4 o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (mine) {
+      // pieces in order: piece i is warp i % e.z of CTA i / e.z
+      const int first = blockIdx.x * e.z + k, last = e.x, lc = last / e.z;
+      const int n1 = e.y & 1 ? 1 : min(last, (int)(blockIdx.x + 1) * e.z - 1) - first + 1;
+      const int nm = max(0, lc - (int)blockIdx.x - 1);
+      const int n = n1 + nm + (lc == (int)blockIdx.x ? 0 : e.y & 2 ? 1 : last - lc * e.z + 1);
+      for (int i0 = sub; i0 < n; i0 += per * U) {
+        float2 ml[U];
+        float4 w[U][V];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * per;
+          ml[u] = make_float2(kNoRef, 0.f);
+          if (i >= n) continue;
+          const int slot = i < n1        ? (e.y & 1 ? 2 * c0 : 2 * (c0 + k + i) + (i == 0 ? 1 : 0))
+                           : i < n1 + nm ? 2 * WARPS * ((int)blockIdx.x + 1 + i - n1)
+                                         : 2 * (lc * WARPS + i - n1 - nm);
+          const int64_t at = (int64_t)slot * R + row;
+          ml[u] = p.ws_ml[at];
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            if (v * 128 + lane * 4 < D) w[u][v] = *reinterpret_cast<const float4 *>(p.ws_o + at * D + v * 128 + lane * 4);
+        }
+        float now = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) now = fmaxf(now, ml[u].x);
+        const float f0 = ex2_approx(m - now);
+        m = now;
+        l *= f0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          o[v].x *= f0;
+          o[v].y *= f0;
+          o[v].z *= f0;
+          o[v].w *= f0;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (i0 + u * per >= n || saw_none(ml[u].x, ml[u].y)) continue;
+          const float f = ex2_approx(ml[u].x - m);
+          l = fmaf(f, ml[u].y, l);
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            o[v].x = fmaf(f, w[u][v].x, o[v].x);
+            o[v].y = fmaf(f, w[u][v].y, o[v].y);
+            o[v].z = fmaf(f, w[u][v].z, o[v].z);
+            o[v].w = fmaf(f, w[u][v].w, o[v].w);
+          }
+        }
+      }
+    }
+    if (per > 1) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v * 128 + lane * 4 < D) *reinterpret_cast<float4 *>(&part[warp][v * 128 + lane * 4]) = o[v];
+      if (lane == 0) part_ml[warp] = make_float2(m, l);
+      __syncthreads();
+      if (mine && sub == 0) {
+        float now = m;
+        for (int w = 1; w < per; ++w) now = fmaxf(now, part_ml[warp + w].x);
+        const float f0 = saw_none(m, l) ? 0.f : ex2_approx(m - now);
+        m = now;
+        l *= f0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          o[v].x *= f0;
+          o[v].y *= f0;
+          o[v].z *= f0;
+          o[v].w *= f0;
+        }
+        for (int w = 1; w < per; ++w) {
+          const float2 ml = part_ml[warp + w];
+          if (saw_none(ml.x, ml.y)) continue;
+          const float f = ex2_approx(ml.x - m);
+          l = fmaf(f, ml.y, l);
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            if (v * 128 + lane * 4 >= D) break;
+            const float4 u = *reinterpret_cast<const float4 *>(&part[warp + w][v * 128 + lane * 4]);
+            o[v].x = fmaf(f, u.x, o[v].x);
+            o[v].y = fmaf(f, u.y, o[v].y);
+            o[v].z = fmaf(f, u.z, o[v].z);
+            o[v].w = fmaf(f, u.w, o[v].w);
+          }
+        }
+      }
+    }
+    if (mine && sub == 0) {
+      const bool none = saw_none(m, l);
+      const float inv = none ? 0.f : 1.f / l;
+      const int64_t at = out_row(p, d.x, d.y, d.z + row);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v * 128 + lane * 4 < D)
+          *reinterpret_cast<uint2 *>(p.o + at * D + v * 128 + lane * 4) =
+              make_uint2(pack_bf16x2(o[v].x * inv, o[v].y * inv), pack_bf16x2(o[v].z * inv, o[v].w * inv));
+      if (lane == 0) p.lse[at] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+    if (per > 1) __syncthreads();  // the shared sums are free again
+  }
 }
 
-// CTAs of a variant that one SM holds, on each device; sets the kernel's
-// shared-memory limit on the first call there.
+// Sets a variant's shared-memory limit on its first call on a device.
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 
-template <int G, int R>
-cudaError_t resident(int device, int *out) {
-  static int known[kMaxDevices];
+template <typename S>
+cudaError_t prepare(int device) {
+  static bool done[kMaxDevices];
   std::lock_guard<std::mutex> lock(g_mu);
-  if (known[device] == 0) {
-    constexpr int smem = Kv4Shape<G, R>::SMEM;
-    cudaError_t e = cudaFuncSetAttribute(attn_kv4_kernel<G, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (!done[device]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(attn_kv4_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
-    int n = 0;
-    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kv4_kernel<G, R>, THREADS, smem)) != cudaSuccess)
-      return e;
-    known[device] = n < 1 ? 1 : n;
+    done[device] = true;
   }
-  *out = known[device];
   return cudaSuccess;
 }
 
-template <int G, int R>
+template <typename S>
 int launch_kv4(Kv4Params &p, int device, int sms, cudaStream_t st) {
-  constexpr int D = G * kKv4Group;
-  int per_sm = 0;
-  cudaError_t e = resident<G, R>(device, &per_sm);
+  cudaError_t e = prepare<S>(device);
   if (e != cudaSuccess) return record_cuda_error(e);
-  // no more CTAs than there can be tiles
-  const int64_t rows = (int64_t)p.T * p.group, row_tiles = rows / R + p.B;
-  const int64_t tiles = (((int64_t)p.max_pages << p.shift) + TK - 1) / TK + START;
-  const int64_t most = row_tiles * p.H * (tiles < 1 ? 1 : tiles);
-  int grid = sms * (KV4_CTAS ? KV4_CTAS : per_sm);
-  if (grid > kMaxGrid) grid = kMaxGrid;
-  if (grid > most) grid = (int)most;
-  const size_t o_bytes = (size_t)grid * 2 * R * D * 4, ml_bytes = (size_t)grid * 2 * R * 8;
+  // one CTA per SM, and no more pieces than there can be units
+  const int64_t row_tiles = (int64_t)p.T * p.group / S::R + p.B;
+  const int64_t tiles = ((int64_t)p.max_pages * S::P + S::TK - 1) / S::TK + 1 + S::START;
+  const int64_t most = (row_tiles * p.H * tiles + S::WARPS - 1) / S::WARPS;
+  const int grid = (int)(most < sms ? most : sms);
+  p.pieces = grid * S::WARPS;
+  const size_t o_bytes = (size_t)p.pieces * 2 * S::R * S::D * 4, ml_bytes = (size_t)p.pieces * 2 * S::R * 8;
   uint8_t *ws = nullptr;
-  if (scratch_alloc(reinterpret_cast<void **>(&ws), o_bytes + ml_bytes + (size_t)grid * 32, st) != cudaSuccess || !ws) {
+  if (scratch_alloc(reinterpret_cast<void **>(&ws), o_bytes + ml_bytes + (size_t)p.pieces * 32, st) != cudaSuccess ||
+      !ws) {
     cudaGetLastError();
     return ATTN_ERR_NOMEM;
   }
   p.ws_o = reinterpret_cast<float *>(ws);
   p.ws_ml = reinterpret_cast<float2 *>(ws + o_bytes);
   p.ws_cut = reinterpret_cast<int4 *>(ws + o_bytes + ml_bytes);
-  attn_kv4_kernel<G, R><<<grid, THREADS, Kv4Shape<G, R>::SMEM, st>>>(p);
+  attn_kv4_kernel<S><<<(unsigned)grid, S::THREADS, S::SMEM, st>>>(p);
   e = cudaGetLastError();
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid, R);
+    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -861,11 +1084,25 @@ int launch_kv4(Kv4Params &p, int device, int sms, cudaStream_t st) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attn_kv4_merge_kernel<G>, (const Kv4Params)p, (int)R);
+    e = cudaLaunchKernelEx(&cfg, attn_kv4_merge_kernel<S>, (const Kv4Params)p);
   }
   const cudaError_t f = cudaFreeAsync(ws, st);
   if (e == cudaSuccess) e = f;
   return e == cudaSuccess ? ATTN_OK : record_cuda_error(e);
+}
+
+template <int P>
+int launch_page_size(Kv4Params &p, int G, bool wide, int device, int sms, cudaStream_t st) {
+  switch (G) {
+    case 1:
+      return wide ? launch_kv4<Shape<1, 16, P>>(p, device, sms, st) : launch_kv4<Shape<1, 8, P>>(p, device, sms, st);
+    case 2:
+      return wide ? launch_kv4<Shape<2, 16, P>>(p, device, sms, st) : launch_kv4<Shape<2, 8, P>>(p, device, sms, st);
+    case 3:
+      return launch_kv4<Shape<3, 8, P>>(p, device, sms, st);
+    default:
+      return launch_kv4<Shape<4, 8, P>>(p, device, sms, st);
+  }
 }
 
 bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
@@ -908,18 +1145,15 @@ int attn_fwd_kv4(const void *q, long long q_stride_t, long long q_stride_h, cons
   p.max_pages = num_pages > 0 ? max_pages : 0;  // without pages no request holds a token
   p.B = B; p.T = T; p.H = Hkv; p.group = Hq / Hkv; p.shift = shift; p.causal = causal;
   p.scale_log2 = scale * kLog2e;
-  p.chunk_min = KV4_MIN;
-  p.wait_limit = wait_limit_ns();
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // 16 rows a tile where the requests have more than 8 on average: K and V
   // are then read and unpacked once for 16 rows; at D > 128 the accumulators
   // of 16 rows would not leave registers for a second CTA on the SM
   const bool wide = (int64_t)p.group * ((T + B - 1) / B) > 8;
-  switch (D / 64) {
-    case 1: return wide ? launch_kv4<1, 16>(p, device, sms, st) : launch_kv4<1, 8>(p, device, sms, st);
-    case 2: return wide ? launch_kv4<2, 16>(p, device, sms, st) : launch_kv4<2, 8>(p, device, sms, st);
-    case 3: return launch_kv4<3, 8>(p, device, sms, st);
-    default: return launch_kv4<4, 8>(p, device, sms, st);
+  switch (page_size) {
+    case 16: return launch_page_size<16>(p, D / 64, wide, device, sms, st);
+    case 32: return launch_page_size<32>(p, D / 64, wide, device, sms, st);
+    default: return launch_page_size<64>(p, D / 64, wide, device, sms, st);
   }
 }
 
