@@ -45,6 +45,8 @@ def library_path() -> str:
 def load_library() -> ctypes.CDLL:
     """Load libattn_gb300.so once; raise if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

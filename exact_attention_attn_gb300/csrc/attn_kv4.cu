@@ -115,7 +115,7 @@ struct Shape {
   static constexpr int STAGE = PAGES * PAGE_BYTES;
   // Warps of a CTA (one CTA per SM), as the registers allow: 128 a thread for
   // 64 dims, 168 for 128 dims or 16 rows of 64, 255 for more.
-  static constexpr int WARPS = G == 1 ? (R == 8 ? 16 : 12) : G == 2 && R == 8 ? KV4_W2 : G == 4 && P == 64 ? 6 : 8;
+  static constexpr int WARPS = G == 1 ? (R == 8 ? 16 : 12) : G == 2 && R == 8 ? (P == 64 ? 12 : KV4_W2) : G == 4 && P == 64 ? 6 : 8;
   static constexpr int THREADS = WARPS * 32;
   // as many stages as the SM's shared memory holds, 8 at most
   static constexpr int FIT = 221184 / (WARPS * STAGE);

@@ -22,69 +22,89 @@ import torch
 from .binding import ATTN_OK, AttnError, load_library
 
 _GROUP = 64
-_Strides = ctypes.c_longlong * 3
+_BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+# A decode step's kernels take a few microseconds, so the calls here are written to cost the host little: each tensor's
+# usual form is recognised with a handful of attribute reads, and only another form goes through the checks that say
+# what is wrong with it (or that it is fine).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_strides = {}
 
 
-class _On:
-    """The tensors' device made current, and the stream's handle."""
-    __slots__ = ("device", "stream", "guard", "handle")
-
-    def __init__(self, device, stream):
-        self.device, self.stream, self.guard = device, stream, None
-
-    def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        s = torch.cuda.current_stream() if self.stream is None else self.stream
-        self.handle = s.cuda_stream if hasattr(s, "cuda_stream") else int(s)
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
-
-    def keep(self, *tensors):
-        """Allocated here for the current stream, used on another one."""
-        if self.stream is not None and isinstance(self.stream, torch.cuda.Stream):
-            for t in tensors:
-                t.record_stream(self.stream)
+def _strides3(s):
+    """The ctypes array of three strides; one array a value, kept for the next call."""
+    a = _strides.get(s)
+    if a is None:
+        if len(_strides) >= 4096:
+            _strides.clear()
+        a = _strides[s] = (ctypes.c_longlong * 3)(*s)
+    return a
 
 
-def _cuda(t, name, dtype, ndim, device=None):
+def _run(fn, what, index, stream, made, *args):
+    """fn(*args, stream) with the tensors' device current.  ``made``: tensors
+    allocated here for the current stream, which may be used on another one."""
+    if stream is None and index == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            s = torch.cuda.current_stream() if stream is None else stream
+            rc = fn(*args, s.cuda_stream if hasattr(s, "cuda_stream") else int(s))
+        if isinstance(stream, torch.cuda.Stream):
+            for t in made:
+                t.record_stream(stream)
+    if rc != ATTN_OK:
+        raise AttnError(rc, what)
+
+
+def _cuda(t, name, dtype, ndim, index=None):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got shape {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
 
 
-def _dense(t, name, dtype, ndim, device=None):
-    _cuda(t, name, dtype, ndim, device)
+def _dense(t, name, dtype, shape, index):
+    """A contiguous tensor of a known shape."""
+    if t.dtype is dtype and t.get_device() == index and t.is_contiguous() and t.shape == shape:
+        return
+    _cuda(t, name, dtype, len(shape), index)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _dims_last(t, name):
-    """The strides before the last dim, in elements; a dim of size one has none that matters."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+def _last_dim(t, name):
+    """The strides before the last dim, in elements (0 for a dim of size one: it is never stepped along)."""
+    s = t.stride()
+    if 1 in t.shape:
+        if t.shape[-1] > 1 and s[-1] != 1:
+            raise ValueError(f"{name}'s last dim must be contiguous")
+        return tuple(0 if n == 1 else x for n, x in zip(t.shape[:-1], s[:-1]))
+    if s[-1] != 1:
         raise ValueError(f"{name}'s last dim must be contiguous")
-    return [0 if n == 1 else s for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+    return s[:-1]
 
 
-def _written(t, name):
+def _written(strides, shape, name):
     """A tensor that is written must not hold an element twice (an expanded dim)."""
-    if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+    if 0 in strides and any(n > 1 and x == 0 for n, x in zip(shape, strides)):
         raise ValueError(f"{name} is written and must not be expanded")
 
 
-def _done(rc, what):
-    if rc != ATTN_OK:
-        raise AttnError(rc, what)
+def _rows(table, index):
+    """The row stride of a block table [B, max_pages]."""
+    _cuda(table, "table", _I32, 2, index)
+    s, n = table.stride(), table.shape
+    if n[1] > 1 and s[1] != 1:
+        raise ValueError("table's last dim must be contiguous")
+    if n[0] > 1:
+        return s[0]
+    return max(n[1], 1)
 
 
 # ---------------------------------------------------------------- rotary positions
@@ -120,54 +140,59 @@ def attn_rope_table(rot_dim: int, sections=None, base: float = 10000.0, inv_freq
     if rot_dim % 2 or len(axis) != n or len(freq) != n:
         raise ValueError(f"rot_dim {rot_dim} needs {n} frequencies: sections have {len(axis)}, inv_freq {len(freq)}")
     host = torch.empty((n, 2), dtype=torch.int64)
-    axes = max(axis, default=0) + 1
-    _done(load_library().attn_rope_table((ctypes.c_double * n)(*freq), (ctypes.c_int * n)(*axis), n, axes,
-                                         host.data_ptr()), "attn_rope_table")
+    rc = load_library().attn_rope_table((ctypes.c_double * n)(*freq), (ctypes.c_int * n)(*axis), n, max(axis, default=0) + 1,
+                                        host.data_ptr())
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_rope_table")
     return host.to(device)
 
 
 def _rope(q, k, positions, table, adjacent, out_q, out_k, backward, stream, what):
-    lib = load_library()
-    dev = q.device
-    _cuda(q, "q", torch.bfloat16, 4)
+    index = q.get_device()
+    _cuda(q, "q", _BF16, 4)
     B, Hq, N, D = q.shape
-    _cuda(positions, "positions", torch.int32, 3, dev)
-    if positions.shape[1] != B or positions.shape[2] != N:
-        raise ValueError(f"positions {tuple(positions.shape)} do not match [axes, {B}, {N}]")
+    _cuda(positions, "positions", _I32, 3, index)
+    axes, b, n = positions.shape
     ps = positions.stride()
+    if b != B or n != N:
+        raise ValueError(f"positions {tuple(positions.shape)} do not match [axes, {B}, {N}]")
     if N > 1 and ps[2] != 1:
         raise ValueError("positions' last dim must be contiguous")
-    _dense(table, "table", torch.int64, 2, dev)
-    if table.shape[1] != 2:
-        raise ValueError(f"table must be [rot_dim / 2, 2], got {tuple(table.shape)}")
-    pairs, made = [], []
-    for x, out, name in ((q, out_q, "q"), (k, out_k, "k")):
-        if x is None:
-            if out is not None:
-                raise ValueError(f"out_{name} without {name}")
-            pairs.append((None, None, None, None, 0, None))
-            continue
-        if x is not q:
-            _cuda(x, name, torch.bfloat16, 4, dev)
-            if x.shape[0] != B or x.shape[2] != N or x.shape[3] != D:
-                raise ValueError(f"k {tuple(x.shape)} does not match q {tuple(q.shape)}")
-        if out is None:
-            out = torch.empty_like(x)
-            made.append(out)
-        else:
-            _cuda(out, "out_" + name, torch.bfloat16, 4, dev)
-            if out.shape != x.shape:
-                raise ValueError(f"out_{name} {tuple(out.shape)} does not match {tuple(x.shape)}")
-        _written(out, "out_" + name)
-        pairs.append((x.data_ptr(), _Strides(*_dims_last(x, name)), out.data_ptr(),
-                      _Strides(*_dims_last(out, "out_" + name)), x.shape[1], out))
-    with _On(dev, stream) as on:
-        on.keep(*made)
-        rc = lib.attn_rope(*pairs[0][:5], *pairs[1][:5], positions.data_ptr(), ps[0], ps[1] if B > 1 else 0,
-                           positions.shape[0], table.data_ptr(), B, N, D, 2 * table.shape[0], 1 if adjacent else 0,
-                           backward, on.handle)
-    _done(rc, what)
-    return pairs[0][5], pairs[1][5]
+    half = table.shape[0]
+    _dense(table, "table", _I64, (half, 2), index)
+    made = []
+    if out_q is None:
+        out_q = torch.empty_like(q)
+        made.append(out_q)
+    elif out_q is not q:
+        _cuda(out_q, "out_q", _BF16, 4, index)
+        if out_q.shape != q.shape:
+            raise ValueError(f"out_q {tuple(out_q.shape)} does not match {tuple(q.shape)}")
+    so = _last_dim(out_q, "out_q")
+    _written(so, out_q.shape, "out_q")
+    first = (q.data_ptr(), _strides3(_last_dim(q, "q")), out_q.data_ptr(), _strides3(so), Hq)
+    if k is None:
+        if out_k is not None:
+            raise ValueError("out_k without k")
+        second = (None, None, None, None, 0)
+    else:
+        _cuda(k, "k", _BF16, 4, index)
+        shape = k.shape
+        if shape[0] != B or shape[2] != N or shape[3] != D:
+            raise ValueError(f"k {tuple(shape)} does not match q {tuple(q.shape)}")
+        if out_k is None:
+            out_k = torch.empty_like(k)
+            made.append(out_k)
+        elif out_k is not k:
+            _cuda(out_k, "out_k", _BF16, 4, index)
+            if out_k.shape != shape:
+                raise ValueError(f"out_k {tuple(out_k.shape)} does not match {tuple(shape)}")
+        so = _last_dim(out_k, "out_k")
+        _written(so, shape, "out_k")
+        second = (k.data_ptr(), _strides3(_last_dim(k, "k")), out_k.data_ptr(), _strides3(so), shape[1])
+    _run(load_library().attn_rope, what, index, stream, made, *first, *second, positions.data_ptr(), ps[0],
+         ps[1] if B > 1 else 0, axes, table.data_ptr(), B, N, D, 2 * half, 1 if adjacent else 0, backward)
+    return out_q, out_k
 
 
 def attn_rope(q, k, positions, table, adjacent: bool = False, out_q=None, out_k=None, stream=None):
@@ -186,45 +211,36 @@ def attn_rope_bwd(dq, dk, positions, table, adjacent: bool = False, out_q=None, 
 
 # ---------------------------------------------------------------- pages
 
-def _table(t, dev=None):
-    _cuda(t, "table", torch.int32, 2, dev)
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError("table's last dim must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
-
-
-def _int_outs(dev, want, out):
-    """The int32 outputs by name: given ones checked, the others made."""
+def _int_outs(like, want, out):
+    """The int32 outputs by name (``want``: their lengths): given ones checked, the others made."""
     got, made = {}, []
-    unknown = set(out or ()) - set(want)
-    if unknown:
-        raise ValueError(f"unknown outputs {sorted(unknown)}")
+    if out:
+        index = like.get_device()
+        for name in out:
+            if name not in want:
+                raise ValueError(f"unknown output {name!r}")
     for name, n in want.items():
-        t = (out or {}).get(name)
+        t = out.get(name) if out else None
         if t is None:
-            t = torch.empty(n, dtype=torch.int32, device=dev)
+            t = torch.empty(n, dtype=_I32, device=like.device)
             made.append(t)
         else:
-            _dense(t, name, torch.int32, 1, dev)
-            if t.shape[0] != n:
-                raise ValueError(f"{name} must have {n} elements, got {t.shape[0]}")
+            _dense(t, name, _I32, (n,), index)
         got[name] = t
     return got, made
 
 
 def _page_state(table, lens, arg, arg_name, free_pages, free_count):
-    stride = _table(table)
-    _written(table, "table")
-    dev, B = table.device, table.shape[0]
-    for t, name in ((lens, "lens"), (arg, arg_name)):
-        _dense(t, name, torch.int32, 1, dev)
-        if t.shape[0] != B:
-            raise ValueError(f"{name} must have {B} elements (rows of table), got {t.shape[0]}")
-    _dense(free_pages, "free_pages", torch.int32, 1, dev)
-    _dense(free_count, "free_count", torch.int32, 1, dev)
-    if free_count.shape[0] != 1:
-        raise ValueError("free_count must have one element")
-    return stride, dev, B
+    index = table.get_device()
+    stride = _rows(table, None)
+    B, width = table.shape
+    _written(table.stride(), table.shape, "table")
+    _dense(lens, "lens", _I32, (B,), index)
+    _dense(arg, arg_name, _I32, (B,), index)
+    capacity = free_pages.shape[0]
+    _dense(free_pages, "free_pages", _I32, (capacity,), index)
+    _dense(free_count, "free_count", _I32, (1,), index)
+    return stride, index, B, width, capacity
 
 
 def attn_pages_assign(table, lens, new_lens, free_pages, free_count, page_size: int, max_tokens: int, out=None,
@@ -238,17 +254,13 @@ def attn_pages_assign(table, lens, new_lens, free_pages, free_count, page_size: 
     the step was refused and nothing changed, see ATTN_PAGES_* in
     include/attn.h).  ``out`` may hold any of them; out["lens"] may be lens and
     out["free_count"] free_count, for updates in place."""
-    stride, dev, B = _page_state(table, lens, new_lens, "new_lens", free_pages, free_count)
-    o, made = _int_outs(dev, {"lens": B, "free_count": 1, "cu": B + 1, "slots": max_tokens, "positions": max_tokens,
-                              "info": 2}, out)
-    with _On(dev, stream) as on:
-        on.keep(*made)
-        rc = load_library().attn_pages_assign(
-            table.data_ptr(), stride, table.shape[1], lens.data_ptr(), new_lens.data_ptr(), B, page_size,
-            free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(), o["lens"].data_ptr(),
-            o["free_count"].data_ptr(), o["cu"].data_ptr(), o["slots"].data_ptr(), o["positions"].data_ptr(),
-            max_tokens, o["info"].data_ptr(), on.handle)
-    _done(rc, "attn_pages_assign")
+    stride, index, B, width, capacity = _page_state(table, lens, new_lens, "new_lens", free_pages, free_count)
+    o, made = _int_outs(table, {"lens": B, "free_count": 1, "cu": B + 1, "slots": max_tokens, "positions": max_tokens,
+                                "info": 2}, out)
+    _run(load_library().attn_pages_assign, "attn_pages_assign", index, stream, made, table.data_ptr(), stride, width,
+         lens.data_ptr(), new_lens.data_ptr(), B, page_size, free_pages.data_ptr(), capacity, free_count.data_ptr(),
+         o["lens"].data_ptr(), o["free_count"].data_ptr(), o["cu"].data_ptr(), o["slots"].data_ptr(),
+         o["positions"].data_ptr(), max_tokens, o["info"].data_ptr())
     return o
 
 
@@ -256,15 +268,12 @@ def attn_pages_release(table, lens, keep_lens, free_pages, free_count, page_size
     """Requests cut to ``keep_lens`` tokens (0: finished; negative: left alone),
     their pages back on the stack.  ``table`` and ``free_pages`` are updated in
     place; returns a dict of lens [B], free_count [1] and info [2]."""
-    stride, dev, B = _page_state(table, lens, keep_lens, "keep_lens", free_pages, free_count)
-    o, made = _int_outs(dev, {"lens": B, "free_count": 1, "info": 2}, out)
-    with _On(dev, stream) as on:
-        on.keep(*made)
-        rc = load_library().attn_pages_release(
-            table.data_ptr(), stride, table.shape[1], lens.data_ptr(), keep_lens.data_ptr(), B, page_size,
-            free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(), o["lens"].data_ptr(),
-            o["free_count"].data_ptr(), o["info"].data_ptr(), on.handle)
-    _done(rc, "attn_pages_release")
+    stride, index, B, width, capacity = _page_state(table, lens, keep_lens, "keep_lens", free_pages, free_count)
+    _written(free_pages.stride(), free_pages.shape, "free_pages")
+    o, made = _int_outs(table, {"lens": B, "free_count": 1, "info": 2}, out)
+    _run(load_library().attn_pages_release, "attn_pages_release", index, stream, made, table.data_ptr(), stride, width,
+         lens.data_ptr(), keep_lens.data_ptr(), B, page_size, free_pages.data_ptr(), capacity, free_count.data_ptr(),
+         o["lens"].data_ptr(), o["free_count"].data_ptr(), o["info"].data_ptr())
     return o
 
 
@@ -283,58 +292,59 @@ def attn_kv4_cache(num_pages: int, Hkv: int, head_dim: int, page_size: int, devi
     return torch.zeros((num_pages, Hkv, attn_kv4_page_bytes(head_dim, page_size)), dtype=torch.uint8, device=device)
 
 
-def _cache_dim(cache, page_size, dev=None):
-    """Head dim of a cache: a page holds 72 bytes per token and group of 64 dims."""
-    _dense(cache, "cache", torch.uint8, 3, dev)
-    per = 72 * page_size
-    if page_size < 1 or cache.shape[2] == 0 or cache.shape[2] % per:
+def _cache(cache, page_size):
+    """Device, pages, kv heads and head dim of a cache: a page holds 72 bytes per token and group of 64 dims."""
+    pages, heads, size = cache.shape if cache.dim() == 3 else (0, 0, 0)
+    if not (cache.dtype is _U8 and cache.is_contiguous() and cache.dim() == 3):
+        _cuda(cache, "cache", _U8, 3)
+        raise ValueError("cache must be contiguous")
+    if page_size < 1 or size == 0 or size % (72 * page_size):
         raise ValueError(f"cache {tuple(cache.shape)} is not one of pages of {page_size} tokens")
-    return cache.shape[2] // per * _GROUP
+    return cache.get_device(), pages, heads, size // (72 * page_size) * _GROUP
+
+
+def _view(t, name, shape, index):
+    """The strides of a bf16 [.., .., D] view of a known shape."""
+    if not (t.dtype is _BF16 and t.shape == shape and t.get_device() == index):
+        _cuda(t, name, _BF16, 3, index)
+        raise ValueError(f"{name} {tuple(t.shape)} does not match {tuple(shape)}")
+    return _last_dim(t, name)
 
 
 def attn_kv4_append(k, v, slots, cache, page_size: int, stream=None) -> None:
     """Quantises k and v (bf16 [T, Hkv, D], any strides with a contiguous last
     dim) into the cache's slots (int32 [T]; -1 skips a token; no slot twice)."""
-    D = _cache_dim(cache, page_size)
-    dev = cache.device
-    _cuda(k, "k", torch.bfloat16, 3, dev)
-    _cuda(v, "v", torch.bfloat16, 3, dev)
-    _dense(slots, "slots", torch.int32, 1, dev)
-    T, H = slots.shape[0], cache.shape[1]
-    if k.shape != v.shape or tuple(k.shape) != (T, H, D):
-        raise ValueError(f"k {tuple(k.shape)} / v {tuple(v.shape)} do not match [{T}, {H}, {D}]")
-    ks, vs = _dims_last(k, "k"), _dims_last(v, "v")
-    with _On(dev, stream) as on:
-        rc = load_library().attn_kv4_append(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], slots.data_ptr(),
-                                            cache.data_ptr(), cache.shape[0], T, H, D, page_size, on.handle)
-    _done(rc, "attn_kv4_append")
+    index, pages, H, D = _cache(cache, page_size)
+    if index < 0:
+        _cuda(cache, "cache", _U8, 3)
+    T = slots.shape[0]
+    _dense(slots, "slots", _I32, (T,), index)
+    ks, vs = _view(k, "k", (T, H, D), index), _view(v, "v", (T, H, D), index)
+    _run(load_library().attn_kv4_append, "attn_kv4_append", index, stream, (), k.data_ptr(), ks[0], ks[1], v.data_ptr(),
+         vs[0], vs[1], slots.data_ptr(), cache.data_ptr(), pages, T, H, D, page_size)
 
 
 def attn_kv4_read(slots, cache, page_size: int, out_k=None, out_v=None, stream=None):
     """K and V of the slots (int32 [T]) as bf16 [Hkv, T, D]: k[None], v[None]
     are attn_fwd's operands for a cached prefix.  Slot -1 reads as zeros."""
-    D = _cache_dim(cache, page_size)
-    dev = cache.device
-    _dense(slots, "slots", torch.int32, 1, dev)
-    T, H = slots.shape[0], cache.shape[1]
-    made, outs = [], []
-    for t, name in ((out_k, "out_k"), (out_v, "out_v")):
-        if t is None:
-            t = torch.empty((H, T, D), dtype=torch.bfloat16, device=dev)
-            made.append(t)
-        else:
-            _cuda(t, name, torch.bfloat16, 3, dev)
-            if tuple(t.shape) != (H, T, D):
-                raise ValueError(f"{name} {tuple(t.shape)} does not match [{H}, {T}, {D}]")
-            _written(t, name)
-        outs.append(t)
-    ks, vs = _dims_last(outs[0], "out_k"), _dims_last(outs[1], "out_v")
-    with _On(dev, stream) as on:
-        on.keep(*made)
-        rc = load_library().attn_kv4_read(cache.data_ptr(), cache.shape[0], slots.data_ptr(), outs[0].data_ptr(), ks[0],
-                                          ks[1], outs[1].data_ptr(), vs[0], vs[1], T, H, D, page_size, on.handle)
-    _done(rc, "attn_kv4_read")
-    return outs[0], outs[1]
+    index, pages, H, D = _cache(cache, page_size)
+    if index < 0:
+        _cuda(cache, "cache", _U8, 3)
+    T = slots.shape[0]
+    _dense(slots, "slots", _I32, (T,), index)
+    made = []
+    if out_k is None:
+        out_k = torch.empty((H, T, D), dtype=_BF16, device=cache.device)
+        made.append(out_k)
+    if out_v is None:
+        out_v = torch.empty((H, T, D), dtype=_BF16, device=cache.device)
+        made.append(out_v)
+    ks, vs = _view(out_k, "out_k", (H, T, D), index), _view(out_v, "out_v", (H, T, D), index)
+    _written(ks, out_k.shape, "out_k")
+    _written(vs, out_v.shape, "out_v")
+    _run(load_library().attn_kv4_read, "attn_kv4_read", index, stream, made, cache.data_ptr(), pages, slots.data_ptr(),
+         out_k.data_ptr(), ks[0], ks[1], out_v.data_ptr(), vs[0], vs[1], T, H, D, page_size)
+    return out_k, out_v
 
 
 def attn_fwd_kv4(q, cu, lens, table, cache, page_size: int, scale: float | None = None, causal: bool = True, out=None,
@@ -347,40 +357,33 @@ def attn_fwd_kv4(q, cu, lens, table, cache, page_size: int, scale: float | None 
     and lens[r] cached tokens, theirs among them (``causal``: bottom-right
     aligned, as attn_fwd).  Rows outside cu[0] .. cu[B] are left as they were.
     Head dims 64, 128, 192, 256."""
-    D = _cache_dim(cache, page_size)
-    dev = cache.device
-    _cuda(q, "q", torch.bfloat16, 3, dev)
+    index, pages, H, D = _cache(cache, page_size)
+    if index < 0:
+        _cuda(cache, "cache", _U8, 3)
     T, Hq = q.shape[0], q.shape[1]
-    Hkv = cache.shape[1]
-    if q.shape[2] != D:
+    if q.dim() == 3 and q.shape[2] != D:
         raise ValueError(f"q {tuple(q.shape)} does not match the cache's head dim {D}")
-    stride = _table(table, dev)
-    B = table.shape[0]
-    _dense(cu, "cu", torch.int32, 1, dev)
-    _dense(lens, "lens", torch.int32, 1, dev)
-    if cu.shape[0] != B + 1 or lens.shape[0] != B:
+    qs = _view(q, "q", (T, Hq, D), index)
+    stride = _rows(table, index)
+    B, width = table.shape
+    if cu.shape != (B + 1,) or lens.shape != (B,):
         raise ValueError(f"cu {tuple(cu.shape)} / lens {tuple(lens.shape)} do not match {B} requests (rows of table)")
+    _dense(cu, "cu", _I32, (B + 1,), index)
+    _dense(lens, "lens", _I32, (B,), index)
     made = []
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device)
         made.append(out)
     else:
-        _dense(out, "out", torch.bfloat16, 3, dev)
+        _dense(out, "out", _BF16, (T, Hq, D), index)
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        lse = torch.empty((T, Hq), dtype=_F32, device=q.device)
         made.append(lse)
     else:
-        _dense(lse, "lse", torch.float32, 2, dev)
-    if out.shape != q.shape or tuple(lse.shape) != (T, Hq):
-        raise ValueError("out / lse shape mismatch")
+        _dense(lse, "lse", _F32, (T, Hq), index)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    qs = _dims_last(q, "q")
-    with _On(dev, stream) as on:
-        on.keep(*made)
-        rc = load_library().attn_fwd_kv4(q.data_ptr(), qs[0], qs[1], cu.data_ptr(), lens.data_ptr(), table.data_ptr(),
-                                         stride, table.shape[1], cache.data_ptr(), cache.shape[0], out.data_ptr(),
-                                         lse.data_ptr(), B, T, Hq, Hkv, D, page_size, scale, 1 if causal else 0,
-                                         on.handle)
-    _done(rc, "attn_fwd_kv4")
+    _run(load_library().attn_fwd_kv4, "attn_fwd_kv4", index, stream, made, q.data_ptr(), qs[0], qs[1], cu.data_ptr(),
+         lens.data_ptr(), table.data_ptr(), stride, width, cache.data_ptr(), pages, out.data_ptr(), lse.data_ptr(), B, T,
+         Hq, H, D, page_size, scale, 1 if causal else 0)
     return out, lse
