@@ -27,8 +27,8 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxThreads = 1024;
+constexpr int kMaxWarps = kMaxThreads / 32;
 
 struct PagesParams {
   int *table;
@@ -47,7 +47,7 @@ struct PagesParams {
 
 // Exclusive sums of (a, b) over the block's threads; the block totals in ta, tb.
 __device__ __forceinline__ void block_scan(long long &a, long long &b, long long &ta, long long &tb) {
-  __shared__ long long wa[kWarps], wb[kWarps];
+  __shared__ long long wa[kMaxWarps], wb[kMaxWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long ia = a, ib = b;
 #pragma unroll
@@ -65,8 +65,7 @@ __device__ __forceinline__ void block_scan(long long &a, long long &b, long long
   __syncthreads();
   long long pa = 0, pb = 0;
   ta = tb = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
     if (w < warp) {
       pa += wa[w];
       pb += wb[w];
@@ -91,17 +90,17 @@ __device__ __forceinline__ int find_last(const int *sums, int n, int x) {
 }
 
 template <bool ASSIGN>
-__global__ void __launch_bounds__(kThreads) attn_pages_kernel(const PagesParams p) {
+__global__ void __launch_bounds__(kMaxThreads) attn_pages_kernel(const PagesParams p) {
   extern __shared__ int sm[];
   __shared__ int verdict;
   int *tok = sm, *pg = sm + p.B, *len = sm + 2 * p.B;  // first token, first page, length of each request
   const int ncta = gridDim.x, cta = blockIdx.x;
-  const int gt = cta * kThreads + threadIdx.x, gn = ncta * kThreads;
+  const int threads = blockDim.x, gt = cta * threads + threadIdx.x, gn = ncta * threads;
   const int count = *p.free_count;
   const int64_t room = (int64_t)p.max_pages << p.shift;
   int bad = (count < 0 || count > p.free_capacity) ? ATTN_PAGES_BAD_COUNT : 0;
   long long tokens = 0, pages = 0;
-  for (int base = 0; base < p.B; base += kThreads) {
+  for (int base = 0; base < p.B; base += threads) {
     const int r = base + threadIdx.x;
     long long a = 0, b = 0;
     if (r < p.B) {
@@ -171,27 +170,41 @@ __global__ void __launch_bounds__(kThreads) attn_pages_kernel(const PagesParams 
     }
   }
   if constexpr (ASSIGN) {
+    // Four tokens a thread, each looked up by itself so that the four page
+    // loads overlap; 16-byte stores where the buffers allow them.
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15u) == 0;
     for (int64_t i0 = (int64_t)gt * 4; i0 < p.max_tokens; i0 += (int64_t)gn * 4) {
+      int slot[4], pos[4];
       int r = i0 < total ? find_last(tok, p.B, (int)i0) : 0;
-      int end = r + 1 < p.B ? tok[r + 1] : total;
+      const int *from[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int64_t i = i0 + u;
-        if (i >= p.max_tokens) break;
-        int slot = -1, pos = 0;
+        pos[u] = 0;
+        from[u] = nullptr;
         if (i < total) {
-          while (i >= end) {
-            ++r;
-            end = r + 1 < p.B ? tok[r + 1] : total;
-          }
-          pos = len[r] + (int)(i - tok[r]);
-          const int j = pos >> p.shift, have = (int)(((int64_t)len[r] + p.P - 1) >> p.shift);
+          while (r + 1 < p.B && tok[r + 1] <= i) ++r;
+          pos[u] = len[r] + (int)(i - tok[r]);
+          const int j = pos[u] >> p.shift, have = (int)(((int64_t)len[r] + p.P - 1) >> p.shift);
           // a page of this step comes from the stack: its table entry may not be written yet
-          const int page = j < have ? p.table[(int64_t)r * p.table_stride + j] : p.free_pages[count - 1 - (pg[r] + j - have)];
-          slot = page * p.P + (pos & (p.P - 1));
+          from[u] = j < have ? p.table + (int64_t)r * p.table_stride + j : p.free_pages + (count - 1 - (pg[r] + j - have));
         }
-        p.slots[i] = slot;
-        p.positions[i] = pos;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) slot[u] = from[u] ? *from[u] : -1;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (from[u]) slot[u] = slot[u] * p.P + (pos[u] & (p.P - 1));
+      if (wide && i0 + 4 <= p.max_tokens) {
+        *reinterpret_cast<int4 *>(p.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        *reinterpret_cast<int4 *>(p.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (i0 + u < p.max_tokens) {
+            p.slots[i0 + u] = slot[u];
+            p.positions[i0 + u] = pos[u];
+          }
       }
     }
   }
@@ -208,12 +221,15 @@ int launch_pages(PagesParams &p, cudaStream_t st) {
   if (smem > 40 * 1024 && (e = cudaFuncSetAttribute(attn_pages_kernel<ASSIGN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                     (int)(ATTN_PAGES_MAX_REQUESTS * 3 * sizeof(int)))) != cudaSuccess)
     return record_cuda_error(e);
-  // one CTA up to 4 Ki written entries, then one for each 4 Ki, at most 8
-  int64_t n = ASSIGN ? ((int64_t)p.max_tokens + 4095) / 4096 : ((int64_t)p.B + 4095) / 4096;
+  // one CTA of 256 threads for a decode step's few tokens, else CTAs of 1024,
+  // one for each 2 Ki written entries, at most 8
+  const int64_t entries = ASSIGN ? (int64_t)p.max_tokens + p.B : (int64_t)4 * p.B;
+  const int threads = p.B <= 256 && entries <= 1024 ? 256 : kMaxThreads;
+  int64_t n = entries / 2048;
   n = n < 1 ? 1 : n > 8 ? 8 : n;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)n);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
