@@ -31,7 +31,7 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxRot = ATTN_MAX_HEAD_DIM;
 
 struct RopeTensor {
@@ -76,28 +76,30 @@ __global__ void __launch_bounds__(kThreads) attn_rope_kernel(const RopeParams p)
   extern __shared__ float2 cs[];  // [nt][rot / 2]
   const int half = p.rot >> 1, tasks = p.D >> 4, rtasks = p.rot >> 4;
   const int b = blockIdx.x / p.nblocks, n0 = (blockIdx.x % p.nblocks) * p.nt;
+  const int task = threadIdx.x % tasks, rest = threadIdx.x / tasks;
+  const int nl = rest % p.nt, lane = rest / p.nt, n = n0 + nl;
+  const bool active = lane < p.lanes && n < p.N;
+  const bool turn = task < rtasks;
+  // the task's two chunks of 8 dims
+  const int d0 = turn && !ADJ ? task * 8 : task * 16, d1 = turn && !ADJ ? task * 8 + half : task * 16 + 8;
   for (int i = threadIdx.x; i < p.nt * half; i += kThreads) {
-    const int n = n0 + i / half;
-    if (n >= p.N) break;
+    const int m = n0 + i / half;
+    if (m >= p.N) break;
     const longlong2 e = p.table[i % half];
     int axis = (int)e.y;
     if ((unsigned long long)e.y >= (unsigned long long)p.axes) {  // not a table of this call's axes
       atomicCAS(p.status, 0, kStatusDevice);
       axis = 0;
     }
-    const int64_t pos = p.pos[axis * p.pos_a + b * p.pos_b + n];
+    const int64_t pos = p.pos[axis * p.pos_a + b * p.pos_b + m];
     const uint64_t turns = (uint64_t)pos * (uint64_t)e.x;
     float s, c;
     sincospif((float)(int)(turns >> 32) * 0x1p-31f, &s, &c);
     cs[i] = make_float2(c, p.sign * s);
   }
   __syncthreads();
-  const int task = threadIdx.x % tasks, rest = threadIdx.x / tasks;
-  const int nl = rest % p.nt, lane = rest / p.nt, n = n0 + nl;
-  if (lane >= p.lanes || n >= p.N) return;
-  const bool turn = task < rtasks;
+  if (!active) return;
   float c[8], s[8];
-  int d0, d1;  // the task's two chunks of 8 dims
   if (turn) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -105,11 +107,6 @@ __global__ void __launch_bounds__(kThreads) attn_rope_kernel(const RopeParams p)
       c[i] = v.x;
       s[i] = v.y;
     }
-    d0 = ADJ ? task * 16 : task * 8;
-    d1 = ADJ ? task * 16 + 8 : task * 8 + half;
-  } else {
-    d0 = task * 16;
-    d1 = task * 16 + 8;
   }
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
@@ -117,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) attn_rope_kernel(const RopeParams p)
     if (t.heads == 0 || (!turn && t.x == t.y)) continue;  // in place: the passed dims are there already
     const __nv_bfloat16 *x = t.x + b * t.xb + n * t.xn;
     __nv_bfloat16 *y = t.y + b * t.yb + n * t.yn;
-#pragma unroll 2
+#pragma unroll 1
     for (int h = lane; h < t.heads; h += p.lanes) {
       uint4 u = *reinterpret_cast<const uint4 *>(x + h * t.xh + d0);
       uint4 v = *reinterpret_cast<const uint4 *>(x + h * t.xh + d1);
@@ -219,11 +216,14 @@ int attn_rope(const void *q, const long long *q_strides, void *q_out, const long
   p.N = N; p.D = D; p.rot = rot; p.axes = axes; p.adjacent = adjacent;
   p.sign = backward ? -1.f : 1.f;
   p.status = status;
-  // Tokens per CTA: the most (a power of two up to 8) that leaves two CTAs per
-  // SM; one token per CTA where there are few tokens.
+  // Tokens per CTA: the most (a power of two up to 4) that leaves two CTAs per
+  // SM; one token per CTA where there are few tokens.  Measured on q 32 and k 8
+  // heads of 128, N 8192, B 2 (336 MB): CTAs of 128 threads and 4 tokens 56.1 us
+  // (88 % of a plain copy's rate), 256 threads and 8 tokens 57.3, 512 threads
+  // 69.5, 256 threads and 2 tokens 83.1; two heads of a thread in flight 62.5.
   const int tasks = D / 16, fit = kThreads / tasks;
   int nt = 1;
-  while (nt < 8 && nt * 2 <= fit && (int64_t)B * ((N + 2 * nt - 1) / (2 * nt)) >= 2 * sms) nt *= 2;
+  while (nt < 4 && nt * 2 <= fit && (int64_t)B * ((N + 2 * nt - 1) / (2 * nt)) >= 2 * sms) nt *= 2;
   p.nt = nt;
   p.lanes = fit / nt;
   p.nblocks = (N + nt - 1) / nt;

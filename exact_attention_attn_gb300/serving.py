@@ -26,19 +26,25 @@ _BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch
 # A decode step's kernels take a few microseconds, so the calls here are written to cost the host little: each tensor's
 # usual form is recognised with a handful of attribute reads, and only another form goes through the checks that say
 # what is wrong with it (or that it is fine).
+#
+# "Plans": what a call passes on besides its pointers (sizes, strides) depends on its tensors' types, shapes, strides and
+# devices alone.  It is checked and laid out once for each such signature and looked up afterwards.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
-_strides = {}
+_Strides = ctypes.c_longlong * 3
+_plans = {}
 
 
-def _strides3(s):
-    """The ctypes array of three strides; one array a value, kept for the next call."""
-    a = _strides.get(s)
-    if a is None:
-        if len(_strides) >= 4096:
-            _strides.clear()
-        a = _strides[s] = (ctypes.c_longlong * 3)(*s)
-    return a
+def _keep(key, plan):
+    if len(_plans) >= 4096:
+        _plans.clear()
+    _plans[key] = plan
+    return plan
+
+
+def _sig(t):
+    """All of a tensor that a plan may depend on."""
+    return t.dtype, t.get_device(), t.shape, t.stride()
 
 
 def _run(fn, what, index, stream, made, *args):
@@ -147,7 +153,7 @@ def attn_rope_table(rot_dim: int, sections=None, base: float = 10000.0, inv_freq
     return host.to(device)
 
 
-def _rope(q, k, positions, table, adjacent, out_q, out_k, backward, stream, what):
+def _rope_plan(q, k, positions, table, out_q, out_k):
     index = q.get_device()
     _cuda(q, "q", _BF16, 4)
     B, Hq, N, D = q.shape
@@ -160,38 +166,50 @@ def _rope(q, k, positions, table, adjacent, out_q, out_k, backward, stream, what
         raise ValueError("positions' last dim must be contiguous")
     half = table.shape[0]
     _dense(table, "table", _I64, (half, 2), index)
-    made = []
-    if out_q is None:
-        out_q = torch.empty_like(q)
-        made.append(out_q)
-    elif out_q is not q:
-        _cuda(out_q, "out_q", _BF16, 4, index)
-        if out_q.shape != q.shape:
-            raise ValueError(f"out_q {tuple(out_q.shape)} does not match {tuple(q.shape)}")
-    so = _last_dim(out_q, "out_q")
-    _written(so, out_q.shape, "out_q")
-    first = (q.data_ptr(), _strides3(_last_dim(q, "q")), out_q.data_ptr(), _strides3(so), Hq)
+    heads, strides = [], []
+    for x, out, name in ((q, out_q, "q"), (k, out_k, "k")):
+        if x is None:
+            heads.append(0)
+            strides += [None, None]
+            continue
+        _cuda(x, name, _BF16, 4, index)
+        if x.shape[0] != B or x.shape[2] != N or x.shape[3] != D:
+            raise ValueError(f"k {tuple(x.shape)} does not match q {tuple(q.shape)}")
+        _cuda(out, "out_" + name, _BF16, 4, index)
+        if out.shape != x.shape:
+            raise ValueError(f"out_{name} {tuple(out.shape)} does not match {tuple(x.shape)}")
+        so = _last_dim(out, "out_" + name)
+        _written(so, out.shape, "out_" + name)
+        heads.append(x.shape[1])
+        strides += [_Strides(*_last_dim(x, name)), _Strides(*so)]
+    return (index, heads[0], heads[1], *strides, ps[0] if axes > 1 else 0, ps[1] if B > 1 else 0, axes, B, N, D, 2 * half)
+
+
+def _rope(q, k, positions, table, adjacent, out_q, out_k, backward, stream, what):
+    made = ()
+    if out_q is None or (out_k is None and k is not None):
+        _cuda(q, "q", _BF16, 4)
+        made = []
+        if out_q is None:
+            out_q = torch.empty_like(q)
+            made.append(out_q)
+        if out_k is None and k is not None:
+            out_k = torch.empty_like(k)
+            made.append(out_k)
     if k is None:
         if out_k is not None:
             raise ValueError("out_k without k")
-        second = (None, None, None, None, 0)
+        key = (_sig(q), None, _sig(positions), _sig(table), _sig(out_q))
     else:
-        _cuda(k, "k", _BF16, 4, index)
-        shape = k.shape
-        if shape[0] != B or shape[2] != N or shape[3] != D:
-            raise ValueError(f"k {tuple(shape)} does not match q {tuple(q.shape)}")
-        if out_k is None:
-            out_k = torch.empty_like(k)
-            made.append(out_k)
-        elif out_k is not k:
-            _cuda(out_k, "out_k", _BF16, 4, index)
-            if out_k.shape != shape:
-                raise ValueError(f"out_k {tuple(out_k.shape)} does not match {tuple(shape)}")
-        so = _last_dim(out_k, "out_k")
-        _written(so, shape, "out_k")
-        second = (k.data_ptr(), _strides3(_last_dim(k, "k")), out_k.data_ptr(), _strides3(so), shape[1])
-    _run(load_library().attn_rope, what, index, stream, made, *first, *second, positions.data_ptr(), ps[0],
-         ps[1] if B > 1 else 0, axes, table.data_ptr(), B, N, D, 2 * half, 1 if adjacent else 0, backward)
+        key = (_sig(q), _sig(k), _sig(positions), _sig(table), _sig(out_q), _sig(out_k))
+    plan = _plans.get(key) or _keep(key, _rope_plan(q, k, positions, table, out_q, out_k))
+    index, hq, hk, qs, qos, ks, kos, pa, pb, axes, B, N, D, rot = plan
+    if k is None:
+        kp = kop = None
+    else:
+        kp, kop = k.data_ptr(), out_k.data_ptr()
+    _run(load_library().attn_rope, what, index, stream, made, q.data_ptr(), qs, out_q.data_ptr(), qos, hq, kp, ks, kop, kos,
+         hk, positions.data_ptr(), pa, pb, axes, table.data_ptr(), B, N, D, rot, 1 if adjacent else 0, backward)
     return out_q, out_k
 
 
@@ -254,9 +272,20 @@ def attn_pages_assign(table, lens, new_lens, free_pages, free_count, page_size: 
     the step was refused and nothing changed, see ATTN_PAGES_* in
     include/attn.h).  ``out`` may hold any of them; out["lens"] may be lens and
     out["free_count"] free_count, for updates in place."""
-    stride, index, B, width, capacity = _page_state(table, lens, new_lens, "new_lens", free_pages, free_count)
-    o, made = _int_outs(table, {"lens": B, "free_count": 1, "cu": B + 1, "slots": max_tokens, "positions": max_tokens,
-                                "info": 2}, out)
+    key = plan = None
+    if out and len(out) == 6:
+        key = ("assign", max_tokens, _sig(table), _sig(lens), _sig(new_lens), _sig(free_pages), _sig(free_count),
+               *out, *map(_sig, out.values()))
+        plan = _plans.get(key)
+    if plan:
+        o, made = out, ()
+    else:
+        plan = _page_state(table, lens, new_lens, "new_lens", free_pages, free_count)
+        o, made = _int_outs(table, {"lens": plan[2], "free_count": 1, "cu": plan[2] + 1, "slots": max_tokens,
+                                    "positions": max_tokens, "info": 2}, out)
+        if key:
+            _keep(key, plan)
+    stride, index, B, width, capacity = plan
     _run(load_library().attn_pages_assign, "attn_pages_assign", index, stream, made, table.data_ptr(), stride, width,
          lens.data_ptr(), new_lens.data_ptr(), B, page_size, free_pages.data_ptr(), capacity, free_count.data_ptr(),
          o["lens"].data_ptr(), o["free_count"].data_ptr(), o["cu"].data_ptr(), o["slots"].data_ptr(),
@@ -294,10 +323,10 @@ def attn_kv4_cache(num_pages: int, Hkv: int, head_dim: int, page_size: int, devi
 
 def _cache(cache, page_size):
     """Device, pages, kv heads and head dim of a cache: a page holds 72 bytes per token and group of 64 dims."""
-    pages, heads, size = cache.shape if cache.dim() == 3 else (0, 0, 0)
-    if not (cache.dtype is _U8 and cache.is_contiguous() and cache.dim() == 3):
-        _cuda(cache, "cache", _U8, 3)
+    _cuda(cache, "cache", _U8, 3)
+    if not cache.is_contiguous():
         raise ValueError("cache must be contiguous")
+    pages, heads, size = cache.shape
     if page_size < 1 or size == 0 or size % (72 * page_size):
         raise ValueError(f"cache {tuple(cache.shape)} is not one of pages of {page_size} tokens")
     return cache.get_device(), pages, heads, size // (72 * page_size) * _GROUP
@@ -314,36 +343,45 @@ def _view(t, name, shape, index):
 def attn_kv4_append(k, v, slots, cache, page_size: int, stream=None) -> None:
     """Quantises k and v (bf16 [T, Hkv, D], any strides with a contiguous last
     dim) into the cache's slots (int32 [T]; -1 skips a token; no slot twice)."""
-    index, pages, H, D = _cache(cache, page_size)
-    if index < 0:
-        _cuda(cache, "cache", _U8, 3)
-    T = slots.shape[0]
-    _dense(slots, "slots", _I32, (T,), index)
-    ks, vs = _view(k, "k", (T, H, D), index), _view(v, "v", (T, H, D), index)
-    _run(load_library().attn_kv4_append, "attn_kv4_append", index, stream, (), k.data_ptr(), ks[0], ks[1], v.data_ptr(),
-         vs[0], vs[1], slots.data_ptr(), cache.data_ptr(), pages, T, H, D, page_size)
+    key = ("append", page_size, _sig(k), _sig(v), _sig(slots), _sig(cache))
+    plan = _plans.get(key)
+    if plan is None:
+        index, pages, H, D = _cache(cache, page_size)
+        T = slots.shape[0]
+        _dense(slots, "slots", _I32, (T,), index)
+        ks, vs = _view(k, "k", (T, H, D), index), _view(v, "v", (T, H, D), index)
+        plan = _keep(key, (index, *ks, *vs, pages, T, H, D))
+    index, kt, kh, vt, vh, pages, T, H, D = plan
+    _run(load_library().attn_kv4_append, "attn_kv4_append", index, stream, (), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+         slots.data_ptr(), cache.data_ptr(), pages, T, H, D, page_size)
 
 
 def attn_kv4_read(slots, cache, page_size: int, out_k=None, out_v=None, stream=None):
     """K and V of the slots (int32 [T]) as bf16 [Hkv, T, D]: k[None], v[None]
     are attn_fwd's operands for a cached prefix.  Slot -1 reads as zeros."""
-    index, pages, H, D = _cache(cache, page_size)
-    if index < 0:
-        _cuda(cache, "cache", _U8, 3)
-    T = slots.shape[0]
-    _dense(slots, "slots", _I32, (T,), index)
-    made = []
-    if out_k is None:
-        out_k = torch.empty((H, T, D), dtype=_BF16, device=cache.device)
-        made.append(out_k)
-    if out_v is None:
-        out_v = torch.empty((H, T, D), dtype=_BF16, device=cache.device)
-        made.append(out_v)
-    ks, vs = _view(out_k, "out_k", (H, T, D), index), _view(out_v, "out_v", (H, T, D), index)
-    _written(ks, out_k.shape, "out_k")
-    _written(vs, out_v.shape, "out_v")
+    made = ()
+    if out_k is None or out_v is None:
+        _, _, H, D = _cache(cache, page_size)
+        made = []
+        if out_k is None:
+            out_k = torch.empty((H, slots.shape[0], D), dtype=_BF16, device=cache.device)
+            made.append(out_k)
+        if out_v is None:
+            out_v = torch.empty((H, slots.shape[0], D), dtype=_BF16, device=cache.device)
+            made.append(out_v)
+    key = ("read", page_size, _sig(slots), _sig(cache), _sig(out_k), _sig(out_v))
+    plan = _plans.get(key)
+    if plan is None:
+        index, pages, H, D = _cache(cache, page_size)
+        T = slots.shape[0]
+        _dense(slots, "slots", _I32, (T,), index)
+        ks, vs = _view(out_k, "out_k", (H, T, D), index), _view(out_v, "out_v", (H, T, D), index)
+        _written(ks, out_k.shape, "out_k")
+        _written(vs, out_v.shape, "out_v")
+        plan = _keep(key, (index, *ks, *vs, pages, T, H, D))
+    index, kh, kt, vh, vt, pages, T, H, D = plan
     _run(load_library().attn_kv4_read, "attn_kv4_read", index, stream, made, cache.data_ptr(), pages, slots.data_ptr(),
-         out_k.data_ptr(), ks[0], ks[1], out_v.data_ptr(), vs[0], vs[1], T, H, D, page_size)
+         out_k.data_ptr(), kh, kt, out_v.data_ptr(), vh, vt, T, H, D, page_size)
     return out_k, out_v
 
 
@@ -357,33 +395,35 @@ def attn_fwd_kv4(q, cu, lens, table, cache, page_size: int, scale: float | None 
     and lens[r] cached tokens, theirs among them (``causal``: bottom-right
     aligned, as attn_fwd).  Rows outside cu[0] .. cu[B] are left as they were.
     Head dims 64, 128, 192, 256."""
-    index, pages, H, D = _cache(cache, page_size)
-    if index < 0:
-        _cuda(cache, "cache", _U8, 3)
-    T, Hq = q.shape[0], q.shape[1]
-    if q.dim() == 3 and q.shape[2] != D:
-        raise ValueError(f"q {tuple(q.shape)} does not match the cache's head dim {D}")
-    qs = _view(q, "q", (T, Hq, D), index)
-    stride = _rows(table, index)
-    B, width = table.shape
-    if cu.shape != (B + 1,) or lens.shape != (B,):
-        raise ValueError(f"cu {tuple(cu.shape)} / lens {tuple(lens.shape)} do not match {B} requests (rows of table)")
-    _dense(cu, "cu", _I32, (B + 1,), index)
-    _dense(lens, "lens", _I32, (B,), index)
-    made = []
-    if out is None:
-        out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device)
-        made.append(out)
-    else:
+    made = ()
+    if out is None or lse is None:
+        _view(q, "q", q.shape, cache.get_device())
+        made = []
+        if out is None:
+            out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+            made.append(out)
+        if lse is None:
+            lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
+            made.append(lse)
+    key = ("fwd", page_size, _sig(q), _sig(cu), _sig(lens), _sig(table), _sig(cache), _sig(out), _sig(lse))
+    plan = _plans.get(key)
+    if plan is None:
+        index, pages, H, D = _cache(cache, page_size)
+        T, Hq = q.shape[0], q.shape[1]
+        if q.dim() == 3 and q.shape[2] != D:
+            raise ValueError(f"q {tuple(q.shape)} does not match the cache's head dim {D}")
+        qs = _view(q, "q", (T, Hq, D), index)
+        stride = _rows(table, index)
+        B, width = table.shape
+        if cu.shape != (B + 1,) or lens.shape != (B,):
+            raise ValueError(f"cu {tuple(cu.shape)} / lens {tuple(lens.shape)} do not match {B} requests (rows of table)")
+        _dense(cu, "cu", _I32, (B + 1,), index)
+        _dense(lens, "lens", _I32, (B,), index)
         _dense(out, "out", _BF16, (T, Hq, D), index)
-    if lse is None:
-        lse = torch.empty((T, Hq), dtype=_F32, device=q.device)
-        made.append(lse)
-    else:
         _dense(lse, "lse", _F32, (T, Hq), index)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    _run(load_library().attn_fwd_kv4, "attn_fwd_kv4", index, stream, made, q.data_ptr(), qs[0], qs[1], cu.data_ptr(),
+        plan = _keep(key, (index, *qs, stride, width, pages, B, T, Hq, H, D, 1.0 / math.sqrt(D)))
+    index, qt, qh, stride, width, pages, B, T, Hq, H, D, usual = plan
+    _run(load_library().attn_fwd_kv4, "attn_fwd_kv4", index, stream, made, q.data_ptr(), qt, qh, cu.data_ptr(),
          lens.data_ptr(), table.data_ptr(), stride, width, cache.data_ptr(), pages, out.data_ptr(), lse.data_ptr(), B, T,
-         Hq, H, D, page_size, scale, 1 if causal else 0)
+         Hq, H, D, page_size, usual if scale is None else scale, 1 if causal else 0)
     return out, lse
