@@ -134,6 +134,11 @@ struct Shape {
   static_assert(STAGES * STAGE >= R * D * 4, "a warp's part of a shared item fits its ring");
 };
 
+// a / b for a >= 0, b > 0; in 32 bits where both fit, a third of the operations.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return (a | b) >> 31 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // What a request's tiles look like, from the device arrays, with whatever
 // they hold brought into range (reported once through the status word).
 struct Request {
@@ -157,12 +162,16 @@ __device__ __forceinline__ Request load_request(const Kv4Params &p, int r) {
   return q;
 }
 
+// A place in the line of units: unit `off` of the item (request r, head h, row tile rt).
+struct Place {
+  int r, h, rt, off;
+};
+
 // A warp's piece of the line of units, and the item that holds the first unit
 // of its CTA's pieces.
 struct Piece {
   int64_t begin, end, chunk, total;
-  int r;            // request that holds unit `begin`
-  int64_t base;     // its first unit
+  Place at;         // of unit `begin`
   int64_t cta_begin, cta_end, item_begin, item_end;
   int warps;        // pieces of a CTA
   // one item covers the CTA, and more than one warp has a part of it
@@ -171,18 +180,20 @@ struct Piece {
   __device__ __forceinline__ bool complete(int start) const { return item_begin + start >= cta_begin && item_end == cta_end; }
 };
 
-// All threads of the CTA: each warp's piece, and the request it begins in.
+// All threads of the CTA: each warp's piece, and where it begins.
 template <typename S>
 __device__ __forceinline__ void find_piece(const Kv4Params &p, Piece &pc) {
-  __shared__ int64_t wsum[S::WARPS], found_base[S::WARPS], item[2];
-  __shared__ int wmax[S::WARPS], found_r[S::WARPS];
+  __shared__ int64_t wsum[S::WARPS], item[2];
+  __shared__ int wmax[S::WARPS];
+  __shared__ Place found[S::WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + S::THREADS - 1) / S::THREADS;  // consecutive requests of a thread
   const int r0 = min(tid * per, p.B), r1 = min(r0 + per, p.B);
   int64_t mine = 0;
   int longest = 0;
+  Request q{};
   for (int r = r0; r < r1; ++r) {
-    const Request q = load_request<S>(p, r);
+    q = load_request<S>(p, r);
     mine += q.units(p.H, S::START);
     longest = max(longest, q.tiles);
   }
@@ -207,46 +218,47 @@ __device__ __forceinline__ void find_piece(const Kv4Params &p, Piece &pc) {
   }
   // equal pieces, but none so small that one item would be cut into more than
   // kMostParts CTAs: their merging would cost more than the tiles
-  const int64_t chunk = max(max((total + p.pieces - 1) / p.pieces, (int64_t)kLeastUnits),
+  const int64_t chunk = max(max(divide(total + p.pieces - 1, p.pieces), (int64_t)kLeastUnits),
                             (int64_t)((longest + kMostParts * S::WARPS - 1) / (kMostParts * S::WARPS)));
   // where there are few pieces they are spread over the CTAs
-  const int64_t used = (total + chunk - 1) / chunk;
+  const int64_t used = divide(total + chunk - 1, chunk);
   const int warps = (int)min((int64_t)S::WARPS, (used + gridDim.x - 1) / gridDim.x);
   const int64_t at = before + inc - mine;
-  if (mine > 0) {
-#pragma unroll
-    for (int w = 0; w < S::WARPS; ++w) {
-      const int64_t begin = ((int64_t)blockIdx.x * warps + w) * chunk;
-      if (w >= warps || begin < at || begin >= at + mine) continue;
-      int64_t a = at;
-      for (int r = r0; r < r1; ++r) {
-        const Request q = load_request<S>(p, r);
-        const int64_t n = q.units(p.H, S::START);
-        if (begin < a + n) {
-          found_r[w] = r;
-          found_base[w] = a;
-          if (w == 0) {
-            const int64_t i = (begin - a) / (q.tiles + S::START);
-            item[0] = a + i * (q.tiles + S::START);
-            item[1] = item[0] + q.tiles + S::START;
-          }
-          break;
+  const int64_t cta_begin = (int64_t)blockIdx.x * warps * chunk;
+  if (mine > 0 && at < cta_begin + warps * chunk && at + mine > cta_begin) {  // some of the thread's requests are here
+    int64_t a = at;
+    for (int r = r0; r < r1; ++r) {
+      if (per > 1) q = load_request<S>(p, r);
+      const int64_t n = q.units(p.H, S::START);
+      const int each = q.tiles + S::START;
+#pragma unroll 1
+      for (int w = 0; w < warps; ++w) {
+        const int64_t begin = cta_begin + w * chunk;
+        if (begin < a || begin >= a + n) continue;
+        const int64_t i = divide(begin - a, each);
+        Place f;
+        f.r = r;
+        f.off = (int)(begin - a - i * each);
+        f.h = (int)divide(i, q.rt);
+        f.rt = (int)(i - (int64_t)f.h * q.rt);
+        found[w] = f;
+        if (w == 0) {
+          item[0] = begin - f.off;
+          item[1] = begin - f.off + each;
         }
-        a += n;
       }
+      a += n;
     }
   }
   __syncthreads();
   pc.chunk = chunk;
   pc.total = total;
   pc.warps = warps;
-  pc.cta_begin = min((int64_t)blockIdx.x * warps * chunk, total);
+  pc.cta_begin = min(cta_begin, total);
   pc.cta_end = min(pc.cta_begin + warps * chunk, total);
   pc.begin = min(pc.cta_begin + warp * chunk, pc.cta_end);
   pc.end = min(pc.begin + chunk, pc.cta_end);
-  const bool any = pc.begin < pc.end;
-  pc.r = any ? found_r[warp] : 0;
-  pc.base = any ? found_base[warp] : 0;
+  pc.at = pc.begin < pc.end ? found[warp] : Place{};
   pc.item_begin = pc.cta_begin < total ? item[0] : 0;
   pc.item_end = pc.cta_begin < total ? item[1] : 0;
 }
@@ -259,48 +271,53 @@ struct Item {
   int64_t end;    // the item's last unit + 1, in the line
   // last visible key + 1 of row `row` (rows count query token x group head)
   __device__ __forceinline__ int limit(int row, const Kv4Params &p) const {
-    const int i = row / p.group;
+    const int i = row < p.group ? 0 : row / p.group;
     return p.causal ? min(q.len, max(0, i + 1 + q.len - q.nq)) : q.len;
   }
 };
 
 struct Walk {
-  int64_t at, end, base;
-  int r;
+  int64_t begin;   // of the place, in the line
+  int left;        // units of the piece from there on
+  Place at;
   Request q;
   template <typename S>
   __device__ __forceinline__ void start(const Kv4Params &p, const Piece &pc) {
-    at = pc.begin;
-    end = pc.end;
-    base = pc.base;
-    r = pc.r;
-    if (at < end) q = load_request<S>(p, r);
+    begin = pc.begin;
+    left = (int)(pc.end - pc.begin);
+    at = pc.at;
+    if (left > 0) q = load_request<S>(p, at.r);
   }
-  // Next item of the piece; false at its end.
+  // Next item of the piece that has a tile in it; false at its end.
   template <typename S>
   __device__ __forceinline__ bool next(const Kv4Params &p, Item &it) {
-    while (at < end) {
-      while (at >= base + q.units(p.H, S::START)) {  // also steps over requests without query tokens
-        base += q.units(p.H, S::START);
-        if (++r >= p.B) return false;
-        q = load_request<S>(p, r);
+    while (left > 0) {
+      while (at.h == p.H || q.rt == 0) {  // also steps over requests without query tokens
+        if (++at.r >= p.B) return false;
+        q = load_request<S>(p, at.r);
+        at.h = at.rt = at.off = 0;
       }
-      const int64_t local = at - base;
-      const int per = q.tiles + S::START;
-      const int64_t item = local / per;
-      const int off = (int)(local - item * per), n = (int)min((int64_t)(per - off), end - at);
-      const int tile0 = max(0, off - S::START), tile1 = max(0, off + n - S::START);
-      at += n;
-      if (tile0 == tile1) continue;  // no tile of the item itself: it begins in the next piece
+      const int each = q.tiles + S::START, n = min(each - at.off, left);
+      const int tile0 = max(0, at.off - S::START), tile1 = max(0, at.off + n - S::START);
       it.q = q;
-      it.r = r;
+      it.r = at.r;
+      it.h = at.h;
+      it.rt = at.rt;
       it.tile0 = tile0;
-      it.h = (int)(item / q.rt);
-      it.rt = (int)(item - (int64_t)it.h * q.rt);
       it.n = tile1 - tile0;
-      it.end = at - n - off + per;
+      it.end = begin - at.off + each;
       it.whole = it.n == q.tiles;
-      return true;
+      left -= n;
+      begin += n;
+      at.off += n;
+      if (at.off == each) {
+        at.off = 0;
+        if (++at.rt == q.rt) {
+          at.rt = 0;
+          ++at.h;
+        }
+      }
+      if (tile1 > tile0) return true;  // (else no tile of the item itself: it begins in the next piece)
     }
     return false;
   }
@@ -308,7 +325,7 @@ struct Walk {
 
 // Output row (token x query head) of row q of an item whose first query token is t0.
 __device__ __forceinline__ int64_t out_row(const Kv4Params &p, int t0, int h, int q) {
-  const int i = q / p.group;
+  const int i = q < p.group ? 0 : q / p.group;
   return (int64_t)(t0 + i) * (p.H * p.group) + h * p.group + (q - i * p.group);
 }
 
@@ -487,7 +504,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
 #pragma unroll
       for (int j = 0; j < G; ++j) w[j][0] = w[j][1] = make_uint4(0, 0, 0, 0);
       if (row < rows) {
-        const int i = row / p.group, hg = row - i * p.group;
+        const int i = row < p.group ? 0 : row / p.group, hg = row - i * p.group;
         const __nv_bfloat16 *src =
             p.q + (int64_t)(it.q.t0 + i) * p.qt + (int64_t)(it.h * p.group + hg) * p.qh + t * 8;
 #pragma unroll
@@ -510,7 +527,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
       // 2^e scales the row (e in [-114, 126]; zero, subnormal and infinite rows stay in range)
       const int e = min(126, 14 - exp_of(fmaxf(big, 0x1p-112f)));
-      const float up = pow2(e);
+      const float up = pow2(e), up16 = pow2(e - 4);
       float qs[G];
 #pragma unroll
       for (int j = 0; j < G; ++j) {
@@ -520,16 +537,16 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
           float v[8];
           const uint32_t ws[4] = {w[j][k].x, w[j][k].y, w[j][k].z, w[j][k].w};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 4; ++c) {  // odd dims over 16: their nibbles carry that factor
             v[2 * c] = __uint_as_float(ws[c] << 16) * up;
-            v[2 * c + 1] = __uint_as_float(ws[c] & 0xffff0000u) * up;
-            qs[j] += v[2 * c] + v[2 * c + 1];
+            v[2 * c + 1] = __uint_as_float(ws[c] & 0xffff0000u) * up16;
+            qs[j] = fmaf(v[2 * c + 1], 16.f, qs[j] + v[2 * c]);
           }
-          // nibbles (0, 4) and (1, 5), then (2, 6) and (3, 7); odd nibbles carry a factor 16
+          // nibbles (0, 4) and (1, 5), then (2, 6) and (3, 7)
           qb[nt][j][2 * k][0] = half2_bits(v[0], v[4]);
-          qb[nt][j][2 * k][1] = half2_bits(v[1] * 0.0625f, v[5] * 0.0625f);
+          qb[nt][j][2 * k][1] = half2_bits(v[1], v[5]);
           qb[nt][j][2 * k + 1][0] = half2_bits(v[2], v[6]);
-          qb[nt][j][2 * k + 1][1] = half2_bits(v[3] * 0.0625f, v[7] * 0.0625f);
+          qb[nt][j][2 * k + 1][1] = half2_bits(v[3], v[7]);
         }
         qs[j] += __shfl_xor_sync(0xffffffffu, qs[j], 1);
         qs[j] += __shfl_xor_sync(0xffffffffu, qs[j], 2);
@@ -807,18 +824,19 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
         const int row = nt * 8 + 2 * t + c, q = row0 + row;
         if (q >= rows) continue;
         const bool none = saw_none(ref[nt][c], l[nt][c]);
-        const float inv = whole ? (none ? 0.f : 1.f / l[nt][c]) : 1.f;
+        const float inv = whole ? (none ? 0.f : __frcp_rn(l[nt][c])) : 1.f;
         const int64_t at = out_row(p, done.q.t0, done.h, q);
 #pragma unroll
         for (int j = 0; j < G; ++j) {
-          const float sig = 0x1p24f / isig[j], m = vm[nt][j][c];
+          // 1 / isig, a power of two as isig is
+          const float sig = __uint_as_float((254u << 23) - __float_as_uint(isig[j])), m = vm[nt][j][c];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float o[4];
 #pragma unroll
             for (int d = 0; d < 2; ++d) {
-              o[2 * d] = fmaf(acc[nt][j][2 * k + d][c], sig, m) * inv;
-              o[2 * d + 1] = fmaf(acc[nt][j][2 * k + d][2 + c], sig * 0.0625f, m) * inv;
+              o[2 * d] = fmaf(acc[nt][j][2 * k + d][c] * 0x1p24f, sig, m) * inv;
+              o[2 * d + 1] = fmaf(acc[nt][j][2 * k + d][2 + c] * 0x1p20f, sig, m) * inv;
             }
             const int dim = j * kKv4Group + k * 32 + g * 4;
             if (whole)
