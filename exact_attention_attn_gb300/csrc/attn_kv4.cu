@@ -66,6 +66,9 @@ namespace {
 
 using namespace ptx;
 
+#ifndef KV4_NOALIGN
+#define KV4_NOALIGN
+#endif
 #ifndef KV4_E
 #define KV4_E 3
 #endif
@@ -95,7 +98,7 @@ struct Kv4Params {
   const uint8_t *cache;
   int num_pages, max_pages, B, T, H, group, shift, causal;
   float scale_log2;  // scale * log2 e
-  int pieces;        // warps of the grid
+  int pieces;        // warps of the grid; 0: a CTA for each item, no item is cut
   float *ws_o;       // partial O of cut items: [pieces][2][R][D]
   float2 *ws_ml;     // their reference and l: [pieces][2][R]
   int4 *ws_cut;      // [pieces][2]: the item that each piece leaves unfinished
@@ -179,6 +182,48 @@ struct Piece {
   // ... and all of the item's tiles are in this CTA
   __device__ __forceinline__ bool complete(int start) const { return item_begin + start >= cta_begin && item_end == cta_end; }
 };
+
+// One CTA for each item (few and short ones: spreading them further would cost
+// more in merging than it saves): the warps share the item's tiles, and its
+// parts are merged in shared memory, without a workspace or a second kernel.
+template <typename S>
+__device__ __forceinline__ void find_item(const Kv4Params &p, Piece &pc) {
+  __shared__ Place found;
+  __shared__ int tiles;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) tiles = 0;
+  __syncthreads();
+  if (warp == 0) {  // items before each request, 32 requests at a time
+    int64_t before = 0;
+    for (int base = 0; base < p.B && before <= blockIdx.x; base += 32) {
+      Request q{};
+      if (base + lane < p.B) q = load_request<S>(p, base + lane);
+      const int64_t n = (int64_t)p.H * q.rt;
+      int64_t inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      const int64_t i = (int64_t)blockIdx.x - (before + inc - n);
+      if (i >= 0 && i < n) {
+        found = Place{base + lane, (int)i / q.rt, (int)i % q.rt, 0};
+        tiles = q.tiles;
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  __syncthreads();
+  const int n = tiles, each = (n + S::WARPS - 1) / S::WARPS;  // tiles of a warp
+  const int first = min(warp * each, n), last = min(first + each, n);
+  pc = Piece{};
+  pc.at = found;
+  pc.at.off = S::START + first;
+  pc.begin = pc.at.off;
+  pc.end = S::START + last;
+  pc.chunk = pc.warps = 1;
+  pc.cta_end = pc.item_end = pc.total = n == 0 ? 0 : S::START + n;  // (0: no item is left for this CTA)
+}
 
 // All threads of the CTA: each warp's piece, and where it begins.
 template <typename S>
@@ -445,7 +490,10 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
   Item it;
   {
     Piece pc;
-    find_piece<S>(p, pc);
+    if (p.pieces == 0)
+      find_item<S>(p, pc);
+    else
+      find_piece<S>(p, pc);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     Walk walk;
     walk.start<S>(p, pc);
@@ -897,7 +945,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
       }
     }
   }
-  if (lane == 0) {
+  if (lane == 0 && p.pieces > 0) {
     p.ws_cut[piece * 2] = cut;
     p.ws_cut[piece * 2 + 1] = make_int4(cut_last, cut_flags, pc.warps, 0);
   }
@@ -1074,10 +1122,18 @@ template <typename S>
 int launch_kv4(Kv4Params &p, int device, int sms, cudaStream_t st) {
   cudaError_t e = prepare<S>(device);
   if (e != cudaSuccess) return record_cuda_error(e);
-  // one CTA per SM, and no more pieces than there can be units
+  // What the lengths can be at most: one CTA for each item where these are few
+  // and short, else one per SM, and no more pieces than there can be units.
   const int64_t row_tiles = (int64_t)p.T * p.group / S::R + p.B;
-  const int64_t tiles = ((int64_t)p.max_pages * S::P + S::TK - 1) / S::TK + 1 + S::START;
-  const int64_t most = (row_tiles * p.H * tiles + S::WARPS - 1) / S::WARPS;
+  const int64_t tiles = ((int64_t)p.max_pages * S::P + S::TK - 1) / S::TK + 1;
+  const int64_t items = row_tiles * p.H;
+  if (items <= sms && tiles <= 4 * S::WARPS KV4_NOALIGN) {
+    p.pieces = 0;
+    attn_kv4_kernel<S><<<(unsigned)items, S::THREADS, S::SMEM, st>>>(p);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? ATTN_OK : record_cuda_error(e);
+  }
+  const int64_t most = (items * (tiles + S::START) + S::WARPS - 1) / S::WARPS;
   const int grid = (int)(most < sms ? most : sms);
   p.pieces = grid * S::WARPS;
   const size_t o_bytes = (size_t)p.pieces * 2 * S::R * S::D * 4, ml_bytes = (size_t)p.pieces * 2 * S::R * 8;

@@ -392,3 +392,13 @@ def test_agrees_with_attn_fwd_on_the_values_read_back():
     # K's values move by 2^-8 relative (a score by up to 2^-8 scale sum |q k|, about 0.03 here), V's and both outputs too
     assert (a.float() - b[0].transpose(0, 1).float()).abs().max() <= 0.1
     assert (la - lb[0].T).abs().max() <= 0.1
+
+
+@pytest.mark.parametrize("lens,nq,H,P,D", [((130,), (1,), 1, 16, 64), ((700, 3, 0, 33), (2, 1, 1, 0), 2, 32, 128), ((1500,), (9,), 1, 64, 192),
+                                           ((260,) * 18, (1,) * 18, 8, 16, 64)])
+def test_few_short_items(lens, nq, H, P, D):
+    # a CTA for each item, merged in shared memory: short tables; the same requests under a wide table take the cut
+    # pieces, and both are within the tolerance
+    need = max(-(-n // P) for n in lens)
+    for width in (need, need + 3000 // P):
+        _run(list(lens), list(nq), 4 * H, H, D, P, seed=D, width=width, pad=2)
