@@ -225,7 +225,93 @@ __device__ __forceinline__ void find_item(const Kv4Params &p, Piece &pc) {
   pc.cta_end = pc.item_end = pc.total = n == 0 ? 0 : S::START + n;  // (0: no item is left for this CTA)
 }
 
-// All threads of the CTA: each warp's piece, and where it begins.
+// What follows from the line's length: pieces, and how many of them a CTA has.
+template <typename S>
+__device__ __forceinline__ void set_piece(const Kv4Params &p, int64_t total, int longest, int warp, Piece &pc) {
+  // equal pieces, but none so small that one item would be cut into more than
+  // kMostParts CTAs: their merging would cost more than the tiles
+  const int64_t chunk = max(max(divide(total + p.pieces - 1, p.pieces), (int64_t)kLeastUnits),
+                            (int64_t)((longest + kMostParts * S::WARPS - 1) / (kMostParts * S::WARPS)));
+  // where there are few pieces they are spread over the CTAs
+  int warps = S::WARPS;
+  if (chunk * (p.pieces - (int)gridDim.x) >= total)
+    warps = (int)divide(divide(total + chunk - 1, chunk) + gridDim.x - 1, gridDim.x);
+  pc.chunk = chunk;
+  pc.total = total;
+  pc.warps = warps;
+  pc.cta_begin = min((int64_t)blockIdx.x * warps * chunk, total);
+  pc.cta_end = min(pc.cta_begin + warps * chunk, total);
+  pc.begin = min(pc.cta_begin + warp * chunk, pc.cta_end);
+  pc.end = min(pc.begin + chunk, pc.cta_end);
+}
+
+// The place of unit `at` of the line in request r, whose first unit is `base`.
+template <typename S>
+__device__ __forceinline__ Place place_of(int64_t at, int64_t base, int r, const Request &q) {
+  const int each = q.tiles + S::START;
+  const int64_t i = divide(at - base, each);
+  Place f;
+  f.r = r;
+  f.off = (int)(at - base - i * each);
+  f.h = (int)divide(i, q.rt);
+  f.rt = (int)(i - (int64_t)f.h * q.rt);
+  return f;
+}
+
+// The warp's piece and where it begins, up to 128 requests: every warp looks
+// them all up by itself, four a lane, without waiting for another.
+template <typename S>
+__device__ __forceinline__ void find_piece_few(const Kv4Params &p, Piece &pc) {
+  constexpr int PER = 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (p.B + 31) >> 5, r0 = lane * per;
+  Request q[PER];
+  int64_t mine = 0;
+  int longest = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    q[k] = Request{0, 0, 0, 1, 0};
+    if (k < per && r0 + k < p.B) q[k] = load_request<S>(p, r0 + k);
+  }
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    mine += q[k].units(p.H, S::START);
+    longest = max(longest, q[k].tiles);
+  }
+  int64_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  set_piece<S>(p, __shfl_sync(0xffffffffu, inc, 31), __reduce_max_sync(0xffffffffu, longest), warp, pc);
+  Place mine_at{}, cta_at{};
+  int64_t a = inc - mine;
+  int each = 0;
+  bool has = false, has_cta = false;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int64_t n = q[k].units(p.H, S::START);
+    if (pc.begin >= a && pc.begin < a + n) {
+      mine_at = place_of<S>(pc.begin, a, r0 + k, q[k]);
+      has = true;
+    }
+    if (pc.cta_begin >= a && pc.cta_begin < a + n) {
+      cta_at = place_of<S>(pc.cta_begin, a, r0 + k, q[k]);
+      each = q[k].tiles + S::START;
+      has_cta = true;
+    }
+    a += n;
+  }
+  const unsigned from = __ballot_sync(0xffffffffu, has), cta = __ballot_sync(0xffffffffu, has_cta);
+  const int src = from ? __ffs(from) - 1 : 0, src_cta = cta ? __ffs(cta) - 1 : 0;
+  pc.at = Place{__shfl_sync(0xffffffffu, mine_at.r, src), __shfl_sync(0xffffffffu, mine_at.h, src),
+                __shfl_sync(0xffffffffu, mine_at.rt, src), __shfl_sync(0xffffffffu, mine_at.off, src)};
+  pc.item_begin = cta ? pc.cta_begin - __shfl_sync(0xffffffffu, cta_at.off, src_cta) : 0;
+  pc.item_end = cta ? pc.item_begin + __shfl_sync(0xffffffffu, each, src_cta) : 0;
+}
+
+// The same for any number of requests, by all threads of the CTA together.
 template <typename S>
 __device__ __forceinline__ void find_piece(const Kv4Params &p, Piece &pc) {
   __shared__ int64_t wsum[S::WARPS], item[2];
@@ -236,9 +322,9 @@ __device__ __forceinline__ void find_piece(const Kv4Params &p, Piece &pc) {
   const int r0 = min(tid * per, p.B), r1 = min(r0 + per, p.B);
   int64_t mine = 0;
   int longest = 0;
-  Request q{};
+#pragma unroll 4
   for (int r = r0; r < r1; ++r) {
-    q = load_request<S>(p, r);
+    const Request q = load_request<S>(p, r);
     mine += q.units(p.H, S::START);
     longest = max(longest, q.tiles);
   }
@@ -261,48 +347,26 @@ __device__ __forceinline__ void find_piece(const Kv4Params &p, Piece &pc) {
     total += wsum[w];
     longest = max(longest, wmax[w]);
   }
-  // equal pieces, but none so small that one item would be cut into more than
-  // kMostParts CTAs: their merging would cost more than the tiles
-  const int64_t chunk = max(max(divide(total + p.pieces - 1, p.pieces), (int64_t)kLeastUnits),
-                            (int64_t)((longest + kMostParts * S::WARPS - 1) / (kMostParts * S::WARPS)));
-  // where there are few pieces they are spread over the CTAs
-  const int64_t used = divide(total + chunk - 1, chunk);
-  const int warps = (int)min((int64_t)S::WARPS, (used + gridDim.x - 1) / gridDim.x);
-  const int64_t at = before + inc - mine;
-  const int64_t cta_begin = (int64_t)blockIdx.x * warps * chunk;
-  if (mine > 0 && at < cta_begin + warps * chunk && at + mine > cta_begin) {  // some of the thread's requests are here
-    int64_t a = at;
+  set_piece<S>(p, total, longest, warp, pc);
+  int64_t a = before + inc - mine;
+  if (mine > 0 && a < pc.cta_end && a + mine > pc.cta_begin) {  // some of the thread's requests are here
     for (int r = r0; r < r1; ++r) {
-      if (per > 1) q = load_request<S>(p, r);
+      const Request q = load_request<S>(p, r);
       const int64_t n = q.units(p.H, S::START);
-      const int each = q.tiles + S::START;
 #pragma unroll 1
-      for (int w = 0; w < warps; ++w) {
-        const int64_t begin = cta_begin + w * chunk;
+      for (int w = 0; w < pc.warps; ++w) {
+        const int64_t begin = pc.cta_begin + w * pc.chunk;
         if (begin < a || begin >= a + n) continue;
-        const int64_t i = divide(begin - a, each);
-        Place f;
-        f.r = r;
-        f.off = (int)(begin - a - i * each);
-        f.h = (int)divide(i, q.rt);
-        f.rt = (int)(i - (int64_t)f.h * q.rt);
-        found[w] = f;
+        found[w] = place_of<S>(begin, a, r, q);
         if (w == 0) {
-          item[0] = begin - f.off;
-          item[1] = begin - f.off + each;
+          item[0] = begin - found[w].off;
+          item[1] = item[0] + q.tiles + S::START;
         }
       }
       a += n;
     }
   }
   __syncthreads();
-  pc.chunk = chunk;
-  pc.total = total;
-  pc.warps = warps;
-  pc.cta_begin = min(cta_begin, total);
-  pc.cta_end = min(pc.cta_begin + warps * chunk, total);
-  pc.begin = min(pc.cta_begin + warp * chunk, pc.cta_end);
-  pc.end = min(pc.begin + chunk, pc.cta_end);
   pc.at = pc.begin < pc.end ? found[warp] : Place{};
   pc.item_begin = pc.cta_begin < total ? item[0] : 0;
   pc.item_end = pc.cta_begin < total ? item[1] : 0;
@@ -492,6 +556,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
     Piece pc;
     if (p.pieces == 0)
       find_item<S>(p, pc);
+    else if (p.B <= 128)
+      find_piece_few<S>(p, pc);
     else
       find_piece<S>(p, pc);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
