@@ -32,23 +32,31 @@
 // largest scale, so that its products keep 11 bits down to 2^-24 of the
 // largest.  l and the sums of p m' are in float32.
 //
-// Work split.  The tiles of 32 tokens of all (request, kv head, row tile)
-// items form one line, cut into equal pieces, one per resident warp: lengths
-// are read on the device, and no warp has more than another but for a tile.
-// An item's beginning and end cost a warp about as much as START tiles, so
-// each item is START units longer than its tiles in that line.  A warp works
-// alone -- it copies its own tiles, keeps its own softmax and writes its own
-// result -- so that the latencies of sixteen items overlap on an SM and short
-// requests cost no barrier.  An item cut by a piece's border leaves partial
-// (ref, l, O) in a workspace, at most two per warp, which a second kernel --
-// launched early, its wait overlapping the first's end -- merges in the order
-// of the tokens.
+// Work split.  The tiles of all (request, kv head, row tile) items form one
+// line, cut into equal pieces, one per resident warp: lengths are read on the
+// device, and no warp has more than another but for a tile.  An item's
+// beginning and end cost a warp about as much as START tiles, so each item is
+// START units longer than its tiles in that line (64 requests of 1 to 8192
+// tokens: 49.7 us with 4, 53.9 with 2, 67 with 1).  A warp works alone -- it
+// copies its own tiles, keeps its own softmax and writes its own result -- so
+// that the latencies of an SM's warps overlap and short requests cost no
+// barrier.  An item cut by a piece's border leaves partial (ref, l, O) in a
+// workspace, which a second kernel -- launched early, its wait overlapping the
+// first's end -- merges in the order of the tokens.  Where one item covers all
+// the pieces of a CTA its warps' parts are merged in shared memory first.
+// Where the items are few and short by the sizes alone (no more than SMs, at
+// most 4 tiles a warp), each is one CTA's and there is no second kernel: one
+// request of 129 tokens 6.4 us against 9.8, 8 requests of 1024 11.1 against 14.8.
 //
-// Memory.  Each warp owns a ring of stages of one tile; one bulk copy per page
-// (or, where a page is longer than a tile, per run of rows and pairs in it)
-// fills a stage, and the next tile is asked for as soon as a stage has been
-// read.  Bound: HBM and the issue of instructions, about evenly, for up to 8
-// rows per kv head.
+// Memory.  Each warp owns a ring of stages of one tile (whole pages, 16 bytes
+// a lane and copy), and asks for the next tile as soon as a stage is read.
+//
+// Bound.  Beyond the first 16 us or so of a call the kernel runs at the copy
+// rate of HBM (Hq 32, Hkv 8, D 128: 228 requests of 1024 tokens to 2048, 269 MB
+// more, cost 39.5 us more: 6.8 TB/s); a call's beginning (finding the piece, the
+// first pages, Q), the items' ends and the merge are latency, which is what is
+// left in calls of 100 to 200 MB: 64 requests of 1 to 8192 tokens 4.1 TB/s, one
+// of 131072 3.8 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -66,23 +74,8 @@ namespace {
 
 using namespace ptx;
 
-#ifndef KV4_NOALIGN
-#define KV4_NOALIGN
-#endif
-#ifndef KV4_E
-#define KV4_E 3
-#endif
-#ifndef KV4_PARTS
-#define KV4_PARTS 64
-#endif
-#ifndef KV4_MIN
-#define KV4_MIN 2
-#endif
-#ifndef KV4_W2
-#define KV4_W2 12
-#endif
-constexpr int kMostParts = KV4_PARTS;    // CTAs that one item is cut into, at most
-constexpr int kLeastUnits = KV4_MIN;     // units of a piece, at least
+constexpr int kMostParts = 64;    // CTAs that one item is cut into, at most
+constexpr int kLeastUnits = 2;    // units of a piece, at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoRef = -1e37f;  // reference of a row that has seen no key
@@ -118,14 +111,14 @@ struct Shape {
   static constexpr int STAGE = PAGES * PAGE_BYTES;
   // Warps of a CTA (one CTA per SM), as the registers allow: 128 a thread for
   // 64 dims, 168 for 128 dims or 16 rows of 64, 255 for more.
-  static constexpr int WARPS = G == 1 ? (R == 8 ? 16 : 12) : G == 2 && R == 8 ? (P == 64 ? 12 : KV4_W2) : G == 4 && P == 64 ? 6 : 8;
+  static constexpr int WARPS = G == 1 ? (R == 8 ? 16 : 12) : G == 2 && R == 8 ? 12 : G == 4 && P == 64 ? 6 : 8;
   static constexpr int THREADS = WARPS * 32;
   // as many stages as the SM's shared memory holds, 8 at most
   static constexpr int FIT = 221184 / (WARPS * STAGE);
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int SMEM = WARPS * STAGES * STAGE;
   // An item's beginning and end cost a warp about as much as this many tiles.
-  static constexpr int START = TK == 32 ? KV4_E : (KV4_E + 1) / 2;
+  static constexpr int START = TK == 32 ? 4 : 2;
   // offset of group j's K rows and pairs of a stage's 16 tokens number i
   static constexpr __host__ __device__ int code_row(int i, int j) {
     return P == 16 ? i * PAGE_BYTES + j * P * kKv4RowBytes : (j * P + i * 16) * kKv4RowBytes;
@@ -499,7 +492,6 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // Exponent e of x = f * 2^e, f in [1, 2), for a positive normal x.
 __device__ __forceinline__ int exp_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
 
-
 // The lane's part of the copy of tile `tile` of an item into the stage at
 // `dst`: 16 bytes of every 512.  The pages' ids are in the lanes (lane i: page
 // first + i; page 0 where the request has no further page, whose rows are
@@ -518,7 +510,8 @@ __device__ __forceinline__ void copy_tile(const uint8_t *head, uint32_t page_row
   dst += lane * 16;
 #pragma unroll
   for (int k = 0; k * 32 < CHUNKS; ++k) {
-    const uint8_t *src = k * 32 + 31 < PAGE || S::PAGES == 1 ? src0 : k * 32 >= PAGE ? src1 : k * 32 + lane < PAGE ? src0 : src1;
+    const bool in_first = S::PAGES == 1 || k * 32 + 31 < PAGE || (k * 32 < PAGE && k * 32 + lane < PAGE);
+    const uint8_t *src = in_first ? src0 : src1;
     if (k * 32 + 31 < CHUNKS || k * 32 + lane < CHUNKS) cp_async16(dst + k * 512, src + k * 512);
   }
 }
@@ -700,192 +693,192 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
       __syncwarp();
 #pragma unroll 1
       for (int u = 0; u < TK / 32; ++u) {
-      const int tok0 = tile * TK + u * 32;
-      if (u > 0 && tok0 >= it.q.len) break;
-      const bool edge = tok0 + 32 > full_to, tail = tok0 + 32 > it.q.len;
-      // the first K row of each 16 tokens; everything else is at a fixed distance
-      const uint32_t kc = ring_s + st * S::STAGE + u * (S::code_row(2, 0) - S::code_row(0, 0)) + row_off;
-      const uint32_t km = ring_s + st * S::STAGE + u * (S::pair_row(2, 0) - S::pair_row(0, 0)) + kv4_codes_bytes(G, P) +
-                          g * kKv4PairBytes;
-      // the lane's tokens of S^T: ta, ta + 8 of each 16
-      const int ta = tok0 + g;
+        const int tok0 = tile * TK + u * 32;
+        if (u > 0 && tok0 >= it.q.len) break;
+        const bool edge = tok0 + 32 > full_to, tail = tok0 + 32 > it.q.len;
+        // the first K row of each 16 tokens; everything else is at a fixed distance
+        const uint32_t kc = ring_s + st * S::STAGE + u * (S::code_row(2, 0) - S::code_row(0, 0)) + row_off;
+        const uint32_t km = ring_s + st * S::STAGE + u * (S::pair_row(2, 0) - S::pair_row(0, 0)) + kv4_codes_bytes(G, P) +
+                            g * kKv4PairBytes;
+        // the lane's tokens of S^T: ta, ta + 8 of each 16
+        const int ta = tok0 + g;
 
-      // S^T = K Q^T on the codes, joined over the groups with scales and minima
-      float x[2][NT][4];
+        // S^T = K Q^T on the codes, joined over the groups with scales and minima
+        float x[2][NT][4];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+        for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-        for (int j = 0; j < G; ++j) {
-          uint32_t w[4];  // tokens g and g + 8 of the first 32 dims, then of the others
-          ldmatrix4(w, kc + S::code_row(hf, j));
-          const uint32_t pa = lds32(km + S::pair_row(hf, j)), pb = lds32(km + S::pair_row(hf, j) + 8 * kKv4PairBytes);
-          float s[NT][4];
+          for (int j = 0; j < G; ++j) {
+            uint32_t w[4];  // tokens g and g + 8 of the first 32 dims, then of the others
+            ldmatrix4(w, kc + S::code_row(hf, j));
+            const uint32_t pa = lds32(km + S::pair_row(hf, j)), pb = lds32(km + S::pair_row(hf, j) + 8 * kKv4PairBytes);
+            float s[NT][4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+            for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t xa = w[2 * k], xb = w[2 * k + 1];
+            for (int k = 0; k < 2; ++k) {
+              uint32_t xa = w[2 * k], xb = w[2 * k + 1];
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const uint32_t a0 = xa & 0x000f000fu, a1 = xb & 0x000f000fu, a2 = xa & 0x00f000f0u, a3 = xb & 0x00f000f0u;
+              for (int hh = 0; hh < 2; ++hh) {
+                const uint32_t a0 = xa & 0x000f000fu, a1 = xb & 0x000f000fu, a2 = xa & 0x00f000f0u, a3 = xb & 0x00f000f0u;
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16(s[nt], a0, a1, a2, a3, qb[nt][j][2 * k + hh][0], qb[nt][j][2 * k + hh][1]);
-              xa >>= 8;
-              xb >>= 8;
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_f16(s[nt], a0, a1, a2, a3, qb[nt][j][2 * k + hh][0], qb[nt][j][2 * k + hh][1]);
+                xa >>= 8;
+                xb >>= 8;
+              }
             }
+            const float sa = __uint_as_float(pa << 16), ma = __uint_as_float(pa & 0xffff0000u);
+            const float sb = __uint_as_float(pb << 16), mb = __uint_as_float(pb & 0xffff0000u);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float &xa = x[hf][nt][c], &xb = x[hf][nt][2 + c];
+                xa = fmaf(sa, s[nt][c], j ? fmaf(ma, qsum[nt][j][c], xa) : ma * qsum[nt][j][c]);
+                xb = fmaf(sb, s[nt][2 + c], j ? fmaf(mb, qsum[nt][j][c], xb) : mb * qsum[nt][j][c]);
+              }
           }
-          const float sa = __uint_as_float(pa << 16), ma = __uint_as_float(pa & 0xffff0000u);
-          const float sb = __uint_as_float(pb << 16), mb = __uint_as_float(pb & 0xffff0000u);
+        }
+        // V's scales and minima of the lane's tokens (of those past the request's end none, whatever they are)
+        uint32_t pv[2][G][2];
+        float big_v = 0.f;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int j = 0; j < G; ++j) {
+            const uint32_t vp = km + kv4_side_bytes(G, P) + S::pair_row(hf, j);
+            pv[hf][j][0] = lds32(vp);
+            pv[hf][j][1] = lds32(vp + 8 * kKv4PairBytes);
+            if (tail) {
+              if (ta + hf * 16 >= it.q.len) pv[hf][j][0] = 0u;
+              if (ta + hf * 16 + 8 >= it.q.len) pv[hf][j][1] = 0u;
+            }
+            big_v = max3f(big_v, __uint_as_float(pv[hf][j][0] << 16) * isig[j], __uint_as_float(pv[hf][j][1] << 16) * isig[j]);
+          }
+        // e = y - ref in log2 units; hidden tokens -inf (selected, so that nothing they hold is used)
+        float e[2][NT][4];
+        float top = -INFINITY;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float &xa = x[hf][nt][c], &xb = x[hf][nt][2 + c];
-              xa = fmaf(sa, s[nt][c], j ? fmaf(ma, qsum[nt][j][c], xa) : ma * qsum[nt][j][c]);
-              xb = fmaf(sb, s[nt][2 + c], j ? fmaf(mb, qsum[nt][j][c], xb) : mb * qsum[nt][j][c]);
-            }
-        }
-      }
-      // V's scales and minima of the lane's tokens (of those past the request's end none, whatever they are)
-      uint32_t pv[2][G][2];
-      float big_v = 0.f;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int j = 0; j < G; ++j) {
-          const uint32_t vp = km + kv4_side_bytes(G, P) + S::pair_row(hf, j);
-          pv[hf][j][0] = lds32(vp);
-          pv[hf][j][1] = lds32(vp + 8 * kKv4PairBytes);
-          if (tail) {
-            if (ta + hf * 16 >= it.q.len) pv[hf][j][0] = 0u;
-            if (ta + hf * 16 + 8 >= it.q.len) pv[hf][j][1] = 0u;
-          }
-          big_v = max3f(big_v, __uint_as_float(pv[hf][j][0] << 16) * isig[j], __uint_as_float(pv[hf][j][1] << 16) * isig[j]);
-        }
-      // e = y - ref in log2 units; hidden tokens -inf (selected, so that nothing they hold is used)
-      float e[2][NT][4];
-      float top = -INFINITY;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float &ea = e[hf][nt][c], &eb = e[hf][nt][2 + c];
-            ea = fmaf(x[hf][nt][c], fac[nt][c], -ref[nt][c]);
-            eb = fmaf(x[hf][nt][2 + c], fac[nt][c], -ref[nt][c]);
-            if (edge) {
-              if (ta + hf * 16 >= lim[nt][c]) ea = -INFINITY;
-              if (ta + hf * 16 + 8 >= lim[nt][c]) eb = -INFINITY;
-            }
-            top = max3f(top, ea, eb);
-          }
-      if (__any_sync(0xffffffffu, top > 15.f || big_v > 1.9f)) {  // move the references up
-        float fs[G];
-#pragma unroll
-        for (int j = 0; j < G; ++j) {
-          float big = 0.f;  // from the scales themselves: over the old power of two they may have overflowed
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const float s = __uint_as_float(pv[hf][j][c] << 16);
-              big = fmaxf(big, s < INFINITY ? s : 0.f);
-            }
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-          fs[j] = 1.f;
-          if (big * isig[j] > 1.f) {  // the largest scale becomes [0.5, 1)
-            const float now = pow2(max(-126, -1 - exp_of(big)));
-            fs[j] = now / isig[j];
-            isig[j] = now;
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float m = -INFINITY;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-              for (int u = c; u < 4; u += 2)
-                if (e[hf][nt][u] != -INFINITY) m = fmaxf(m, x[hf][nt][u] * fac[nt][c]);
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float now = fmaxf(ref[nt][c], m - 10.f);
-            const float f = ex2_approx(ref[nt][c] - now);
-            ref[nt][c] = now;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-              for (int u = c; u < 4; u += 2)
-                if (e[hf][nt][u] != -INFINITY) e[hf][nt][u] = fmaf(x[hf][nt][u], fac[nt][c], -now);
-            l[nt][c] *= f;
-#pragma unroll
-            for (int j = 0; j < G; ++j) {
-              vm[nt][j][c] *= f;
-#pragma unroll
-              for (int d = 0; d < 4; ++d) {
-                acc[nt][j][d][c] *= f * fs[j];
-                acc[nt][j][d][2 + c] *= f * fs[j];
+              float &ea = e[hf][nt][c], &eb = e[hf][nt][2 + c];
+              ea = fmaf(x[hf][nt][c], fac[nt][c], -ref[nt][c]);
+              eb = fmaf(x[hf][nt][2 + c], fac[nt][c], -ref[nt][c]);
+              if (edge) {
+                if (ta + hf * 16 >= lim[nt][c]) ea = -INFINITY;
+                if (ta + hf * 16 + 8 >= lim[nt][c]) eb = -INFINITY;
               }
+              top = max3f(top, ea, eb);
             }
-          }
-      }
+        if (__any_sync(0xffffffffu, top > 15.f || big_v > 1.9f)) {  // move the references up
+          float fs[G];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float pr[NT][4];
+          for (int j = 0; j < G; ++j) {
+            float big = 0.f;  // from the scales themselves: over the old power of two they may have overflowed
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            pr[nt][c] = ex2_approx(e[hf][nt][c]);
-            pr[nt][2 + c] = ex2_approx(e[hf][nt][2 + c]);
-            l[nt][c] += pr[nt][c] + pr[nt][2 + c];
-          }
-        // O^T += V^T P^T
-#pragma unroll
-        for (int j = 0; j < G; ++j) {
-          const uint32_t pa = pv[hf][j][0], pb = pv[hf][j][1];
-          const float ua = __uint_as_float(pa << 16) * isig[j], ub = __uint_as_float(pb << 16) * isig[j];
-          const float ma = __uint_as_float(pa & 0xffff0000u), mb = __uint_as_float(pb & 0xffff0000u);
-          uint32_t b0[NT], b1[NT];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float w[4] = {pr[nt][0] * ua, pr[nt][1] * ua, pr[nt][2] * ub, pr[nt][3] * ub};
-            if (!edge) {
-#pragma unroll
-              for (int c = 0; c < 2; ++c) vm[nt][j][c] = fmaf(pr[nt][2 + c], mb, fmaf(pr[nt][c], ma, vm[nt][j][c]));
-            } else {  // a hidden token's scale and minimum may be anything
+            for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const bool no_a = e[hf][nt][c] == -INFINITY, no_b = e[hf][nt][2 + c] == -INFINITY;
-                if (no_a) w[c] = 0.f;
-                if (no_b) w[2 + c] = 0.f;
-                vm[nt][j][c] = fmaf(pr[nt][2 + c], no_b ? 0.f : mb, fmaf(pr[nt][c], no_a ? 0.f : ma, vm[nt][j][c]));
+                const float s = __uint_as_float(pv[hf][j][c] << 16);
+                big = fmaxf(big, s < INFINITY ? s : 0.f);
+              }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+            fs[j] = 1.f;
+            if (big * isig[j] > 1.f) {  // the largest scale becomes [0.5, 1)
+              const float now = pow2(max(-126, -1 - exp_of(big)));
+              fs[j] = now / isig[j];
+              isig[j] = now;
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float m = -INFINITY;
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int u = c; u < 4; u += 2)
+                  if (e[hf][nt][u] != -INFINITY) m = fmaxf(m, x[hf][nt][u] * fac[nt][c]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+              const float now = fmaxf(ref[nt][c], m - 10.f);
+              const float f = ex2_approx(ref[nt][c] - now);
+              ref[nt][c] = now;
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int u = c; u < 4; u += 2)
+                  if (e[hf][nt][u] != -INFINITY) e[hf][nt][u] = fmaf(x[hf][nt][u], fac[nt][c], -now);
+              l[nt][c] *= f;
+#pragma unroll
+              for (int j = 0; j < G; ++j) {
+                vm[nt][j][c] *= f;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                  acc[nt][j][d][c] *= f * fs[j];
+                  acc[nt][j][d][2 + c] *= f * fs[j];
+                }
               }
             }
-            b0[nt] = transpose8x8(half2_bits(w[0], w[1]));
-            b1[nt] = transpose8x8(half2_bits(w[2], w[3]));
-          }
-          uint32_t z[4];  // dims 4g .. 4g + 3 of tokens (2t, 2t + 1) and (8 + 2t, 9 + 2t), then those of the other 32 dims
-          ldmatrix4_trans(z, kc + kv4_side_bytes(G, P) + S::code_row(hf, j));
+        }
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t z0 = z[2 * k], z1 = z[2 * k + 1];
+        for (int hf = 0; hf < 2; ++hf) {
+          float pr[NT][4];
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const uint32_t a0 = z0 & 0x000f000fu, a1 = z0 & 0x00f000f0u, a2 = z1 & 0x000f000fu, a3 = z1 & 0x00f000f0u;
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][j][2 * k + hh], a0, a1, a2, a3, b0[nt], b1[nt]);
-              z0 >>= 8;
-              z1 >>= 8;
+            for (int c = 0; c < 2; ++c) {
+              pr[nt][c] = ex2_approx(e[hf][nt][c]);
+              pr[nt][2 + c] = ex2_approx(e[hf][nt][2 + c]);
+              l[nt][c] += pr[nt][c] + pr[nt][2 + c];
+            }
+          // O^T += V^T P^T
+#pragma unroll
+          for (int j = 0; j < G; ++j) {
+            const uint32_t pa = pv[hf][j][0], pb = pv[hf][j][1];
+            const float ua = __uint_as_float(pa << 16) * isig[j], ub = __uint_as_float(pb << 16) * isig[j];
+            const float ma = __uint_as_float(pa & 0xffff0000u), mb = __uint_as_float(pb & 0xffff0000u);
+            uint32_t b0[NT], b1[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float w[4] = {pr[nt][0] * ua, pr[nt][1] * ua, pr[nt][2] * ub, pr[nt][3] * ub};
+              if (!edge) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) vm[nt][j][c] = fmaf(pr[nt][2 + c], mb, fmaf(pr[nt][c], ma, vm[nt][j][c]));
+              } else {  // a hidden token's scale and minimum may be anything
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  const bool no_a = e[hf][nt][c] == -INFINITY, no_b = e[hf][nt][2 + c] == -INFINITY;
+                  if (no_a) w[c] = 0.f;
+                  if (no_b) w[2 + c] = 0.f;
+                  vm[nt][j][c] = fmaf(pr[nt][2 + c], no_b ? 0.f : mb, fmaf(pr[nt][c], no_a ? 0.f : ma, vm[nt][j][c]));
+                }
+              }
+              b0[nt] = transpose8x8(half2_bits(w[0], w[1]));
+              b1[nt] = transpose8x8(half2_bits(w[2], w[3]));
+            }
+            uint32_t z[4];  // dims 4g .. 4g + 3 of tokens (2t, 2t + 1) and (8 + 2t, 9 + 2t), then those of the other 32 dims
+            ldmatrix4_trans(z, kc + kv4_side_bytes(G, P) + S::code_row(hf, j));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t z0 = z[2 * k], z1 = z[2 * k + 1];
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                const uint32_t a0 = z0 & 0x000f000fu, a1 = z0 & 0x00f000f0u, a2 = z1 & 0x000f000fu, a3 = z1 & 0x00f000f0u;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][j][2 * k + hh], a0, a1, a2, a3, b0[nt], b1[nt]);
+                z0 >>= 8;
+                z1 >>= 8;
+              }
             }
           }
         }
-      }
       }
       __syncwarp();  // every lane has read the stage
       if (asked < stop) {
@@ -1026,13 +1019,13 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
 // The rows of all these items are the CTA's tasks; a warp sums every per-th
 // part of one of them with a running reference, several loads in flight, and
 // the warps of a row are joined through shared memory: a fixed order.
-constexpr int kMergeWarps = 16;
+constexpr int kMergeWarps = 32;
 constexpr int kMergeThreads = kMergeWarps * 32;
 
 template <typename S>
 __global__ void __launch_bounds__(kMergeThreads) attn_kv4_merge_kernel(const Kv4Params p) {
   constexpr int D = S::D, R = S::R, WARPS = S::WARPS, V = (D / 4 + 31) / 32;  // float4s of a lane
-  constexpr int U = V == 1 ? 8 : 4;                        // parts in flight
+  constexpr int U = V == 1 ? 4 : 2;                        // parts in flight
   __shared__ __align__(16) float part[kMergeWarps][D];
   __shared__ float2 part_ml[kMergeWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x * WARPS;
@@ -1051,7 +1044,8 @@ __global__ void __launch_bounds__(kMergeThreads) attn_kv4_merge_kernel(const Kv4
   }
   const int tasks = __shfl_sync(0xffffffffu, sum, 31);
   // warps of a task: the most that leaves every task some
-  const int per = tasks >= 9 ? 1 : tasks >= 5 ? 2 : tasks >= 3 ? 4 : tasks == 2 ? 8 : 16;
+  int per = kMergeWarps;
+  while (per > 1 && tasks * per > kMergeWarps) per >>= 1;
   for (int task0 = 0; task0 < tasks; task0 += kMergeWarps / per) {
     const int task = task0 + warp / per, sub = warp % per;
     const bool mine = task < tasks;
@@ -1193,7 +1187,8 @@ int launch_kv4(Kv4Params &p, int device, int sms, cudaStream_t st) {
   const int64_t row_tiles = (int64_t)p.T * p.group / S::R + p.B;
   const int64_t tiles = ((int64_t)p.max_pages * S::P + S::TK - 1) / S::TK + 1;
   const int64_t items = row_tiles * p.H;
-  if (items <= sms && tiles <= 4 * S::WARPS KV4_NOALIGN) {
+  if (items > ((int64_t)1 << 40) / (tiles + S::START)) return ATTN_ERR_ARG;  // a piece's units are 32-bit
+  if (items <= sms && tiles <= 4 * S::WARPS) {
     p.pieces = 0;
     attn_kv4_kernel<S><<<(unsigned)items, S::THREADS, S::SMEM, st>>>(p);
     e = cudaGetLastError();

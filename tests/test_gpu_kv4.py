@@ -402,3 +402,41 @@ def test_few_short_items(lens, nq, H, P, D):
     need = max(-(-n // P) for n in lens)
     for width in (need, need + 3000 // P):
         _run(list(lens), list(nq), 4 * H, H, D, P, seed=D, width=width, pad=2)
+
+
+def test_offsets_past_32_bits():
+    # pages that lie more than 2^32 bytes into the cache: written, read and attended over as the first ones are
+    H, D, P, n = 8, 128, 16, 150
+    page = H * attn_kv4_page_bytes(D, P)
+    pages = 2 ** 32 // page + 40
+    cache = torch.empty((pages, H, page // H), dtype=torch.uint8, device="cuda")
+    small = attn_kv4_cache(10, H, D, P)
+    k, v, q = _randn((n, H, D), 1), _randn((n, H, D), 2), _randn((1, 32, D), 3)
+    dev = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    far = [pages - 1 - 3 * i for i in range(10)]
+    near = list(range(10))
+    outs = []
+    for c, ids in ((cache, far), (small, near)):
+        slots = dev([ids[t // P] * P + t % P for t in range(n)])
+        attn_kv4_append(k, v, slots, c, P)
+        outs.append((*attn_kv4_read(slots, c, P), *attn_fwd_kv4(q, dev([0, 1]), dev([n]), dev([ids]), c, P)))
+    assert attn_fwd_status() == 0
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    assert torch.equal(cache[far, :, :], small[near, :, :])
+
+
+def test_many_requests():
+    # more requests than one warp looks up by itself (128), some without query tokens or without cached tokens
+    r = np.random.default_rng(3)
+    B = 300
+    lens = [int(x) for x in r.integers(0, 90, B)]
+    nq = [int(min(x, n)) if n else 0 for x, n in zip(r.integers(0, 3, B), lens)]
+    lens[17], nq[17] = 0, 2      # query tokens without a key
+    _run(lens, nq, 4, 2, 64, 16, seed=9, pad=3)
+    _run(lens, nq, 4, 2, 64, 16, seed=9, width=900)
+
+
+@pytest.mark.parametrize("H,g,L", [(1, 8, 30000), (2, 1, 9000), (1, 20, 5000)])
+def test_long_contexts_cut_into_many_parts(H, g, L):
+    _run([L, 40], [1, 2], H * g, H, 128, 32, seed=L, pad=1)

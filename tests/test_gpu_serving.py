@@ -173,3 +173,39 @@ def test_steps_back_to_back_without_waiting():
         o, _ = attn_fwd_kv4(q[i], s.out["cu"], s.lens, s.table, s.cache, P)
         torch.cuda.synchronize()
         assert torch.equal(o[:7], outs[i][:7]), i
+
+
+def test_two_streams_at_once():
+    # the same operators on two streams without waiting for each other: their workspaces are their own
+    a, b = Server(4, 100, 300, 60, seed=70), Server(4, 100, 300, 60, seed=90)
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    for new in ([40, 3, 5, 9], [1, 1, 30, 1], [1, 1, 1, 1]):
+        a.load(new)
+        b.load(new[::-1])
+        torch.cuda.synchronize()
+        a.step(stream=sa)
+        b.step(stream=sb)
+        torch.cuda.synchronize()
+        a.check()
+        b.check()
+
+
+def test_outputs_are_kept_for_the_other_stream():
+    # outputs that the call allocates for a call on another stream are not handed out again before that stream is done
+    s = Server(4, 100, 300, 60, seed=31)
+    s.load([40, 3, 5, 9])
+    s.step()
+    s.check()
+    want, _ = attn_fwd_kv4(s.q, s.out["cu"], s.lens, s.table, s.cache, P)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(20):
+        side.wait_stream(torch.cuda.current_stream())
+        o, lse = attn_fwd_kv4(s.q, s.out["cu"], s.lens, s.table, s.cache, P, stream=side)
+        with torch.cuda.stream(side):
+            got.append(o[:57].clone())
+        del o, lse
+        torch.full_like(s.q, 7.0)  # would land in the freed block
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[:57]) for g in got)
