@@ -17,7 +17,10 @@
 //
 // Eight threads share a group (16 bytes of bfloat16 each, one 4-byte word of
 // codes); 32 consecutive tokens share a CTA, so that a warp writes four
-// neighbouring rows and pairs.  Bound: HBM, 2 + 0.5625 bytes a value.
+// neighbouring rows and pairs.  Bytes: 2 + 0.5625 a value.  Bound: the issue of
+// instructions for append (16384 tokens of 8 heads of 128, 86 MB: 19.4 us, 4.4
+// TB/s, issue slots 74 % busy before the last reduction; 36 us as first written,
+// with divisions), HBM for read (the same 86 MB in 12.7 us, 6.8 TB/s).
 #include <cuda_bf16.h>
 #include <math.h>
 #include <string.h>
@@ -40,6 +43,7 @@ struct AppendParams {
   uint8_t *cache;
   int64_t nslots;
   int T, H, G, shift;
+  int share;  // (head, group) pairs of a CTA
   int *status;
 };
 
@@ -118,7 +122,6 @@ __device__ __forceinline__ void quantise8(const uint4 &w, uint32_t &codes, uint3
   codes = sum - base;
 }
 
-template <int BATCH>
 __global__ void __launch_bounds__(kThreads) attn_kv4_append_kernel(const AppendParams p) {
   const int t = blockIdx.x * kTokens + (threadIdx.x >> 3), sub = threadIdx.x & 7;
   int slot = t < p.T ? p.slots[t] : -1;
@@ -126,40 +129,45 @@ __global__ void __launch_bounds__(kThreads) attn_kv4_append_kernel(const AppendP
     atomicCAS(p.status, 0, kStatusDevice);
     slot = -1;
   }
-  const int P = 1 << p.shift;
-  const int64_t page_bytes = kv4_page_bytes(p.G, P), side = kv4_side_bytes(p.G, P);
-  const int row = slot & (P - 1);
-  uint8_t *page = p.cache + (int64_t)(slot >> p.shift) * p.H * page_bytes;
-  const __nv_bfloat16 *kt = p.k + (int64_t)t * p.kt + sub * 8, *vt = p.v + (int64_t)t * p.vt + sub * 8;
-  // A thread takes BATCH groups at a time, so that their loads are in flight
-  // together.  Lanes without a slot stay for the shuffles, on zeros.
-  const int HG = p.H * p.G;
-  for (int hg0 = blockIdx.y * BATCH; hg0 < HG; hg0 += gridDim.y * BATCH) {
-    uint4 wk[BATCH], wv[BATCH];
-#pragma unroll
-    for (int b = 0; b < BATCH; ++b) {
-      wk[b] = wv[b] = make_uint4(0, 0, 0, 0);
-      const int hg = hg0 + b, h = hg / p.G, g = hg - h * p.G;
-      if (slot >= 0 && hg < HG) {
-        wk[b] = *reinterpret_cast<const uint4 *>(kt + (int64_t)h * p.kh + g * kKv4Group);
-        wv[b] = *reinterpret_cast<const uint4 *>(vt + (int64_t)h * p.vh + g * kKv4Group);
-      }
+  const int P = 1 << p.shift, row = slot & (P - 1), side = kv4_side_bytes(p.G, P);
+  // The CTA's groups, one after the other: (head, group) pairs [hg, end).  The
+  // addresses advance by additions (a multiplication and a division for each
+  // group were a third of the instructions).  Lanes without a slot stay for the
+  // shuffles, on zeros.
+  int hg = blockIdx.y * p.share;
+  const int end = min(hg + p.share, p.H * p.G);
+  int h = hg / p.G, g = hg - h * p.G;
+  const __nv_bfloat16 *k = p.k + (int64_t)t * p.kt + (int64_t)h * p.kh + g * kKv4Group + sub * 8;
+  const __nv_bfloat16 *v = p.v + (int64_t)t * p.vt + (int64_t)h * p.vh + g * kKv4Group + sub * 8;
+  const int64_t k_next = p.kh - (p.G - 1) * kKv4Group, v_next = p.vh - (p.G - 1) * kKv4Group;  // to the next head
+  uint8_t *head = p.cache + ((int64_t)(slot >> p.shift) * p.H + h) * kv4_page_bytes(p.G, P);
+  for (; hg < end; ++hg) {
+    uint4 wk = make_uint4(0, 0, 0, 0), wv = wk;
+    if (slot >= 0) {
+      wk = *reinterpret_cast<const uint4 *>(k);
+      wv = *reinterpret_cast<const uint4 *>(v);
     }
-#pragma unroll
-    for (int b = 0; b < BATCH; ++b) {
-      const int hg = hg0 + b, h = hg / p.G, g = hg - h * p.G;
-      uint32_t ck, pk, cv, pv;
-      quantise8(wk[b], ck, pk);
-      quantise8(wv[b], cv, pv);
-      if (slot < 0 || hg >= HG) continue;
-      uint8_t *at = page + (int64_t)h * page_bytes + (g * P + row) * kKv4RowBytes + sub * 4;
-      uint8_t *pairs = page + (int64_t)h * page_bytes + kv4_codes_bytes(p.G, P) + (g * P + row) * kKv4PairBytes;
-      *reinterpret_cast<uint32_t *>(at) = ck;
-      *reinterpret_cast<uint32_t *>(at + side) = cv;
+    uint32_t ck, pk, cv, pv;
+    quantise8(wk, ck, pk);
+    quantise8(wv, cv, pv);
+    if (slot >= 0) {
+      uint8_t *codes = head + (g * P + row) * kKv4RowBytes + sub * 4;
+      uint8_t *pairs = head + kv4_codes_bytes(p.G, P) + (g * P + row) * kKv4PairBytes;
+      *reinterpret_cast<uint32_t *>(codes) = ck;
+      *reinterpret_cast<uint32_t *>(codes + side) = cv;
       if (sub == 0) {
         *reinterpret_cast<uint32_t *>(pairs) = pk;
         *reinterpret_cast<uint32_t *>(pairs + side) = pv;
       }
+    }
+    if (++g == p.G) {
+      g = 0;
+      k += k_next;
+      v += v_next;
+      head += kv4_page_bytes(p.G, P);
+    } else {
+      k += kKv4Group;
+      v += kKv4Group;
     }
   }
 }
@@ -171,20 +179,29 @@ struct ReadParams {
   int64_t kh, kt, vh, vt;  // element strides of head and token
   int64_t nslots;
   int T, H, G, shift;
+  int share;  // (head, group) pairs of a CTA
   int *status;
 };
 
+// The 8 values of a word of codes.  A code behind the exponent of 2^23 is the
+// float 2^23 + c, so a byte permutation and a subtraction convert it (the
+// conversion instruction has a quarter of their rate).
 __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t pair) {
   const float s = __uint_as_float(pair << 16), m = __uint_as_float(pair & 0xffff0000u);
-  __nv_bfloat162 h[4];
+  const uint64_t s2 = ptx::f2_pack(s, s), m2 = ptx::f2_pack(m, m), bias = ptx::f2_pack(-8388608.f, -8388608.f);
+  const uint32_t even = codes & 0x0f0f0f0fu, odd = (codes >> 4) & 0x0f0f0f0fu;
+  uint32_t out[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float c0 = (float)((codes >> (8 * i)) & 15u), c1 = (float)((codes >> (8 * i + 4)) & 15u);
-    h[i] = __floats2bfloat162_rn(fmaf(c0, s, m), fmaf(c1, s, m));  // c * s is exact: one rounding, then bfloat16's
+    const float c0 = __uint_as_float(__byte_perm(even, 0x4b000000u, 0x7440u + i));
+    const float c1 = __uint_as_float(__byte_perm(odd, 0x4b000000u, 0x7440u + i));
+    // c * s is exact: one rounding, then bfloat16's
+    const uint64_t x = ptx::f2_fma(ptx::f2_add(ptx::f2_pack(c0, c1), bias), s2, m2);
+    float x0, x1;
+    ptx::f2_unpack(x, x0, x1);
+    out[i] = ptx::pack_bf16x2(x0, x1);
   }
-  uint4 w;
-  memcpy(&w, h, sizeof(w));
-  return w;
+  return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 __global__ void __launch_bounds__(kThreads) attn_kv4_read_kernel(const ReadParams p) {
@@ -195,25 +212,36 @@ __global__ void __launch_bounds__(kThreads) attn_kv4_read_kernel(const ReadParam
     atomicCAS(p.status, 0, kStatusDevice);
     slot = -1;
   }
-  const int P = 1 << p.shift;
-  const int64_t page_bytes = kv4_page_bytes(p.G, P), side = kv4_side_bytes(p.G, P);
-  const int row = slot & (P - 1);
-  const uint8_t *page = p.cache + (int64_t)(slot >> p.shift) * p.H * page_bytes;
-  __nv_bfloat16 *kt = p.k + (int64_t)t * p.kt + sub * 8, *vt = p.v + (int64_t)t * p.vt + sub * 8;
-  const int HG = p.H * p.G;
-  for (int hg = blockIdx.y; hg < HG; hg += gridDim.y) {
-    const int h = hg / p.G, g = hg - h * p.G;
+  const int P = 1 << p.shift, row = slot & (P - 1), side = kv4_side_bytes(p.G, P);
+  int hg = blockIdx.y * p.share;
+  const int end = min(hg + p.share, p.H * p.G);
+  int h = hg / p.G, g = hg - h * p.G;
+  __nv_bfloat16 *k = p.k + (int64_t)t * p.kt + (int64_t)h * p.kh + g * kKv4Group + sub * 8;
+  __nv_bfloat16 *v = p.v + (int64_t)t * p.vt + (int64_t)h * p.vh + g * kKv4Group + sub * 8;
+  const int64_t k_next = p.kh - (p.G - 1) * kKv4Group, v_next = p.vh - (p.G - 1) * kKv4Group;  // to the next head
+  const uint8_t *head = p.cache + ((int64_t)(slot >> p.shift) * p.H + h) * kv4_page_bytes(p.G, P);
+#pragma unroll 2
+  for (; hg < end; ++hg) {
     uint32_t ck = 0, cv = 0, pk = 0, pv = 0;  // the pair (0, 0) stands for zeros
     if (slot >= 0) {
-      const uint8_t *at = page + (int64_t)h * page_bytes + (g * P + row) * kKv4RowBytes + sub * 4;
-      const uint8_t *pairs = page + (int64_t)h * page_bytes + kv4_codes_bytes(p.G, P) + (g * P + row) * kKv4PairBytes;
-      ck = *reinterpret_cast<const uint32_t *>(at);
-      cv = *reinterpret_cast<const uint32_t *>(at + side);
+      const uint8_t *codes = head + (g * P + row) * kKv4RowBytes + sub * 4;
+      const uint8_t *pairs = head + kv4_codes_bytes(p.G, P) + (g * P + row) * kKv4PairBytes;
+      ck = *reinterpret_cast<const uint32_t *>(codes);
+      cv = *reinterpret_cast<const uint32_t *>(codes + side);
       pk = *reinterpret_cast<const uint32_t *>(pairs);
       pv = *reinterpret_cast<const uint32_t *>(pairs + side);
     }
-    *reinterpret_cast<uint4 *>(kt + (int64_t)h * p.kh + g * kKv4Group) = values8(ck, pk);
-    *reinterpret_cast<uint4 *>(vt + (int64_t)h * p.vh + g * kKv4Group) = values8(cv, pv);
+    *reinterpret_cast<uint4 *>(k) = values8(ck, pk);
+    *reinterpret_cast<uint4 *>(v) = values8(cv, pv);
+    if (++g == p.G) {
+      g = 0;
+      k += k_next;
+      v += v_next;
+      head += kv4_page_bytes(p.G, P);
+    } else {
+      k += kKv4Group;
+      v += kKv4Group;
+    }
   }
 }
 
@@ -236,13 +264,14 @@ int check_view(const void *x, long long t, long long h) {
   return off16(x) || t % 8 || h % 8 ? ATTN_ERR_ALIGN : ATTN_OK;
 }
 
-// 32 tokens a CTA; the heads' groups are spread over gridDim.y CTAs, as many
-// as give each SM `per_sm` CTAs.
-dim3 cache_grid(int T, int parts, int sms, int per_sm) {
+// 32 tokens a CTA; the (head, group) pairs are spread over gridDim.y CTAs, as
+// many as give each SM 8 CTAs (4 and 16: within 3 % either way).
+dim3 cache_grid(int T, int HG, int sms, int *share) {
   const int x = (T + kTokens - 1) / kTokens;
-  int y = (per_sm * sms + x - 1) / x;
-  y = y < 1 ? 1 : y > parts ? parts : y;
-  return dim3((unsigned)x, (unsigned)y);
+  int y = (8 * sms + x - 1) / x;
+  y = y < 1 ? 1 : y > HG ? HG : y;
+  *share = (HG + y - 1) / y;
+  return dim3((unsigned)x, (unsigned)((HG + *share - 1) / *share));
 }
 
 }  // namespace
@@ -273,14 +302,8 @@ int attn_kv4_append(const void *k, long long k_stride_t, long long k_stride_h, c
   p.cache = static_cast<uint8_t *>(cache);
   p.nslots = (int64_t)num_pages * page_size;
   p.T = T; p.H = Hkv; p.G = D / 64; p.shift = kv4_page_shift(page_size);
-  // Two groups a thread where that still leaves 8 CTAs per SM (16384 tokens of
-  // 8 heads of 128: 20.2 us against 22.1; 64 tokens: 2.9 us against 2.2)
-  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int HG = Hkv * p.G;
-  if ((int64_t)((T + kTokens - 1) / kTokens) * (HG / 2) >= (int64_t)8 * sms)
-    attn_kv4_append_kernel<2><<<cache_grid(T, (HG + 1) / 2, sms, 16), kThreads, 0, st>>>(p);
-  else
-    attn_kv4_append_kernel<1><<<cache_grid(T, HG, sms, 8), kThreads, 0, st>>>(p);
+  const dim3 grid = cache_grid(T, Hkv * p.G, sms, &p.share);
+  attn_kv4_append_kernel<<<grid, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? ATTN_OK : record_cuda_error(e);
 }
@@ -303,7 +326,8 @@ int attn_kv4_read(const void *cache, int num_pages, const int *slots, void *k, l
   p.kh = k_stride_h; p.kt = k_stride_t; p.vh = v_stride_h; p.vt = v_stride_t;
   p.nslots = (int64_t)num_pages * page_size;
   p.T = T; p.H = Hkv; p.G = D / 64; p.shift = kv4_page_shift(page_size);
-  attn_kv4_read_kernel<<<cache_grid(T, Hkv * p.G, sms, 8), kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  const dim3 grid = cache_grid(T, Hkv * p.G, sms, &p.share);
+  attn_kv4_read_kernel<<<grid, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? ATTN_OK : record_cuda_error(e);
 }
