@@ -469,11 +469,17 @@ ATTN_API int attn_kv4_read(const void *cache, int num_pages, const int *slots, v
  * query tokens outside 0 .. T is brought into range (that request's result is
  * then undefined) and attn_fwd_status reports ATTN_ERR_DEVICE.
  *
- * Asynchronous on `stream`: two launches, and a stream-ordered workspace of at
- * most 2048 * (2 * 16 * (D + 2) * 4 + 32) bytes from the library's pool
- * (ATTN_ERR_NOMEM if it cannot be had).  CUDA graphs: as attn_fwd; the grid
- * depends on the sizes alone, so a replay may have other lengths, tables and
- * query counts.  Deterministic for given lengths on a given device.
+ * q, o, lse and cache 16-byte aligned, q_stride_t and q_stride_h multiples of
+ * 8 and >= 0; cu, lens and block_table 4-byte aligned.  (T * Hq / Hkv / 8 + B) *
+ * Hkv * max_pages * page_size / 32 must be below 2^40.
+ *
+ * Asynchronous on `stream`: one launch where the items ((T * Hq / Hkv / 8 + B) *
+ * Hkv by the sizes) are no more than the SMs and max_pages * page_size is a few
+ * hundred tokens to 2048, by head dim; else two launches and a stream-ordered
+ * workspace of at most 21 MB (152 SMs) from the library's pool (ATTN_ERR_NOMEM
+ * if it cannot be had).  CUDA graphs: as attn_fwd; the grid depends on the sizes
+ * alone, so a replay may have other lengths, tables and query counts.
+ * Deterministic for given lengths on a given device.
  */
 #define ATTN_KV4_MAX_REQUESTS 16384
 #define ATTN_KV4_MAX_HEAD_DIM 256
