@@ -1281,10 +1281,13 @@ int attn_fwd_kv4(const void *q, long long q_stride_t, long long q_stride_h, cons
   p.B = B; p.T = T; p.H = Hkv; p.group = Hq / Hkv; p.shift = shift; p.causal = causal;
   p.scale_log2 = scale * kLog2e;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // 16 rows a tile where the requests have more than 8 on average: K and V
-  // are then read and unpacked once for 16 rows; at D > 128 the accumulators
-  // of 16 rows would not leave registers for a second CTA on the SM
-  const bool wide = (int64_t)p.group * ((T + B - 1) / B) > 8;
+  // 16 rows a tile where the requests have more than 64 on average: K and V are
+  // then unpacked once for 16 rows.  With 112 rows (16 heads, 7 tokens, D 64,
+  // 4 requests up to 16384) 33.3 us against 38.2 in tiles of 8, with 256 rows
+  // (2 requests of 8192) 90 against 105; with 64 rows 39.2 against 37.8, with 16
+  // rows 32.6 against 31.3 (fewer warps an SM).  At D > 128 the accumulators of
+  // 16 rows do not fit the registers.
+  const bool wide = (int64_t)p.group * ((T + B - 1) / B) > 64;
   switch (page_size) {
     case 16: return launch_page_size<16>(p, D / 64, wide, device, sms, st);
     case 32: return launch_page_size<32>(p, D / 64, wide, device, sms, st);

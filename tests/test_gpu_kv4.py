@@ -249,6 +249,8 @@ CASES = [
     ((200, 31, 90), (4, 1, 7), 8, 2, 128, 16),
     ((200, 31, 90), (4, 0, 9), 12, 4, 64, 32),
     ((100, 64), (33, 64), 10, 2, 128, 16),
+    ((330, 64, 0, 200), (33, 50, 1, 40), 8, 2, 64, 32),
+    ((500, 77), (40, 70), 8, 2, 128, 64),
     ((70, 40), (5, 3), 16, 1, 256, 16),
     ((5, 3), (9, 3), 4, 2, 64, 16),          # more query tokens than keys: rows that see none
     ((2500,), (1,), 64, 1, 128, 16),
@@ -440,3 +442,11 @@ def test_many_requests():
 @pytest.mark.parametrize("H,g,L", [(1, 8, 30000), (2, 1, 9000), (1, 20, 5000)])
 def test_long_contexts_cut_into_many_parts(H, g, L):
     _run([L, 40], [1, 2], H * g, H, 128, 32, seed=L, pad=1)
+
+
+@pytest.mark.parametrize("P", [16, 32, 64])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_query_tokens(P, D):
+    # more than 64 query rows a request: tiles of 16 rows, one of them ragged, on every page size
+    _run([90, 41, 70], [40, 25, 33], 8, 2, D, P, seed=P + D, width=40)
+    _run([90, 41, 70], [40, 25, 33], 8, 2, D, P, seed=P + D, causal=False, pad=1)
