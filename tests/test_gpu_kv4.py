@@ -450,3 +450,55 @@ def test_many_query_tokens(P, D):
     # more than 64 query rows a request: tiles of 16 rows, one of them ragged, on every page size
     _run([90, 41, 70], [40, 25, 33], 8, 2, D, P, seed=P + D, width=40)
     _run([90, 41, 70], [40, 25, 33], 8, 2, D, P, seed=P + D, causal=False, pad=1)
+
+
+def test_slots_read_twice_and_tokens_before_the_first_request():
+    H, D, P, n = 2, 64, 16, 40
+    cache = _random_cache(3, H, D, P, 21)
+    dev = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    k, v = attn_kv4_read(dev([7, 7, 30, -1, 7]), cache, P)
+    assert torch.equal(k[:, 0], k[:, 1]) and torch.equal(v[:, 0], v[:, 4]) and (k[:, 3] == 0).all()
+    q = _randn((6, 4, D), 22)
+    out, lse = torch.full_like(q, 9.0), torch.full((6, 4), 9.0, device="cuda")
+    attn_fwd_kv4(q, dev([2, 4]), dev([n]), dev([[0, 1, 2]]), cache, P, out=out, lse=lse)
+    assert (out[:2] == 9).all() and (out[4:] == 9).all() and (lse[:2] == 9).all() and (lse[4:] == 9).all()
+    ref, _ = attn_fwd_kv4(q[2:4], dev([0, 2]), dev([n]), dev([[0, 1, 2]]), cache, P)
+    assert torch.equal(out[2:4], ref) and attn_fwd_status() == 0
+
+
+def test_thousands_of_requests_agree_with_a_few_at_a_time():
+    # the lookup of pieces with many requests a thread, against calls of 64 requests (one CTA an item); both are within
+    # half precision's 2^-11 of a weight and one bfloat16 rounding, 2^-8 of the values (at most 6)
+    r = np.random.default_rng(8)
+    B, H, D, P = 5000, 1, 64, 16
+    lens = r.integers(0, 70, B)
+    pages = 600
+    cache = _random_cache(pages, H, D, P, 23)
+    table = torch.tensor(r.integers(0, pages, (B, 5)), dtype=torch.int32, device="cuda")
+    lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    q = _randn((B, 2, D), 24)
+    out, lse = attn_fwd_kv4(q, cu, lens, table, cache, P)
+    assert attn_fwd_status() == 0
+    for a in range(0, B, 64 * 7):
+        b = min(a + 64, B)
+        o, s = attn_fwd_kv4(q[a:b], cu[:b - a + 1], lens[a:b].contiguous(), table[a:b], cache, P)
+        assert (out[a:b].float() - o.float()).abs().max() <= 6 * (2.0 ** -8 + 2.0 ** -10)
+        seen = torch.isfinite(s)
+        assert torch.equal(seen, torch.isfinite(lse[a:b])) and torch.equal(seen[:, 0], lens[a:b] > 0)
+        assert (s[seen] - lse[a:b][seen]).abs().max() <= 2.0 ** -16
+
+
+def test_after_shutdown_and_on_a_stream_handle():
+    from exact_attention_attn_gb300 import attn_shutdown
+    cache = _random_cache(300, 2, 128, 16, 25)
+    dev = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    args = (_randn((1, 8, 128), 26), dev([0, 1]), dev([4700]), dev([list(range(300))]), cache, 16)
+    a, la = attn_fwd_kv4(*args)
+    attn_shutdown()
+    side = torch.cuda.Stream()
+    out, lse = torch.empty_like(a), torch.empty_like(la)
+    torch.cuda.synchronize()
+    attn_fwd_kv4(*args, out=out, lse=lse, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(a, out) and torch.equal(la, lse)

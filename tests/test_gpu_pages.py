@@ -141,3 +141,32 @@ def test_largest_batch():
     dt = _dev(table)
     got = attn_pages_assign(dt, _dev(lens), _dev(new), _dev(free), _dev([B]), P, int(new.sum()))
     _same(got, want, dt, ("lens", "free_count", "cu", "slots", "positions"))
+
+
+def test_assign_and_release_captured():
+    # a captured step replayed on changed lengths, in place; and a release captured behind it
+    B, P, width, cap = 9, 16, 12, 90
+    table, lens, new, keep = _dev(np.full((B, width), -1)), _dev(np.zeros(B)), _dev(np.zeros(B)), _dev(np.full(B, -1))
+    free, count = _dev(np.arange(cap)), _dev([cap])
+    out = {"lens": lens, "free_count": count}
+    out = attn_pages_assign(table, lens, new, free, count, P, 100, out=out)
+    rel = attn_pages_release(table, lens, keep, free, count, P, out={"lens": lens, "free_count": count})
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        attn_pages_assign(table, lens, new, free, count, P, 100, out=out)
+        attn_pages_release(table, lens, keep, free, count, P, out=rel)
+    o_table, o_lens, o_free, o_count = np.full((B, width), -1), np.zeros(B, dtype=np.int64), np.arange(cap), cap
+    r = np.random.default_rng(5)
+    for _ in range(6):
+        n, kp = r.integers(0, 12, B), np.where(r.random(B) < 0.7, -1, r.integers(0, 20, B))
+        new.copy_(_dev(n))
+        keep.copy_(_dev(kp))
+        g.replay()
+        a = S.pages_assign(o_table, o_lens, n, o_free, o_count, P, 100)
+        assert a["info"][0] == 0
+        b = S.pages_release(a["table"], a["lens"], kp, o_free, a["free_count"], P)
+        o_table, o_lens, o_free, o_count = b["table"], b["lens"], b["free"], b["free_count"]
+        assert np.array_equal(out["slots"].cpu().numpy(), a["slots"]) and out["info"].tolist() == a["info"]
+        assert np.array_equal(table.cpu().numpy(), o_table) and np.array_equal(lens.cpu().numpy(), o_lens)
+        assert np.array_equal(free.cpu().numpy(), o_free) and count.item() == o_count and rel["info"].tolist() == b["info"]

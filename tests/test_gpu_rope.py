@@ -139,3 +139,15 @@ def test_rope_empty():
         q = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
         o, _ = attn_rope(q, None, torch.empty((1, shape[0], shape[2]), dtype=torch.int32, device="cuda"), table)
         assert o.shape == shape
+
+
+def test_rope_eight_axes_and_sections_of_nothing():
+    sections = (3, 0, 5, 1, 7, 0, 8, 8)
+    q, k, pos = _inputs(1, 3, 2, 37, 64, 8, 50000, seed=12)
+    inv = [10000.0 ** (-2.0 * i / 64) for i in range(32)]
+    for interleave in (False, True):
+        axis = attn_rope_axes(sections, interleave)
+        oq, ok = attn_rope(q, k, pos, attn_rope_table(64, sections, interleave=interleave))
+        _check(oq, q, pos, inv, axis, False)
+        _check(ok, k, pos, inv, axis, False)
+    assert attn_fwd_status() == 0
