@@ -173,7 +173,9 @@ struct Piece {
   // one item covers the CTA, and more than one warp has a part of it
   __device__ __forceinline__ bool shared() const { return item_end >= cta_end && cta_begin + chunk < cta_end; }
   // ... and all of the item's tiles are in this CTA
-  __device__ __forceinline__ bool complete(int start) const { return item_begin + start >= cta_begin && item_end == cta_end; }
+  __device__ __forceinline__ bool complete(int start) const {
+    return item_begin + start >= cta_begin && item_end == cta_end;
+  }
 };
 
 // One CTA for each item (few and short ones: spreading them further would cost
@@ -720,7 +722,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
               uint32_t xa = w[2 * k], xb = w[2 * k + 1];
 #pragma unroll
               for (int hh = 0; hh < 2; ++hh) {
-                const uint32_t a0 = xa & 0x000f000fu, a1 = xb & 0x000f000fu, a2 = xa & 0x00f000f0u, a3 = xb & 0x00f000f0u;
+                const uint32_t a0 = xa & 0x000f000fu, a1 = xb & 0x000f000fu;
+                const uint32_t a2 = xa & 0x00f000f0u, a3 = xb & 0x00f000f0u;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                   mma_f16(s[nt], a0, a1, a2, a3, qb[nt][j][2 * k + hh][0], qb[nt][j][2 * k + hh][1]);
@@ -754,7 +757,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
               if (ta + hf * 16 >= it.q.len) pv[hf][j][0] = 0u;
               if (ta + hf * 16 + 8 >= it.q.len) pv[hf][j][1] = 0u;
             }
-            big_v = max3f(big_v, __uint_as_float(pv[hf][j][0] << 16) * isig[j], __uint_as_float(pv[hf][j][1] << 16) * isig[j]);
+            big_v = max3f(big_v, __uint_as_float(pv[hf][j][0] << 16) * isig[j],
+                          __uint_as_float(pv[hf][j][1] << 16) * isig[j]);
           }
         // e = y - ref in log2 units; hidden tokens -inf (selected, so that nothing they hold is used)
         float e[2][NT][4];
@@ -863,14 +867,16 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
               b0[nt] = transpose8x8(half2_bits(w[0], w[1]));
               b1[nt] = transpose8x8(half2_bits(w[2], w[3]));
             }
-            uint32_t z[4];  // dims 4g .. 4g + 3 of tokens (2t, 2t + 1) and (8 + 2t, 9 + 2t), then those of the other 32 dims
+            // dims 4g .. 4g + 3 of tokens (2t, 2t + 1) and (8 + 2t, 9 + 2t), then those of the other 32 dims
+            uint32_t z[4];
             ldmatrix4_trans(z, kc + kv4_side_bytes(G, P) + S::code_row(hf, j));
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               uint32_t z0 = z[2 * k], z1 = z[2 * k + 1];
 #pragma unroll
               for (int hh = 0; hh < 2; ++hh) {
-                const uint32_t a0 = z0 & 0x000f000fu, a1 = z0 & 0x00f000f0u, a2 = z1 & 0x000f000fu, a3 = z1 & 0x00f000f0u;
+                const uint32_t a0 = z0 & 0x000f000fu, a1 = z0 & 0x00f000f0u;
+                const uint32_t a2 = z1 & 0x000f000fu, a3 = z1 & 0x00f000f0u;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][j][2 * k + hh], a0, a1, a2, a3, b0[nt], b1[nt]);
                 z0 >>= 8;
@@ -947,7 +953,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
             }
             const int dim = j * kKv4Group + k * 32 + g * 4;
             if (whole)
-              *reinterpret_cast<uint2 *>(p.o + at * D + dim) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+              *reinterpret_cast<uint2 *>(p.o + at * D + dim) =
+                  make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
             else
               *reinterpret_cast<float4 *>(part_o + row * D + dim) = make_float4(o[0], o[1], o[2], o[3]);
           }
@@ -985,7 +992,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
         const float2 ml = warp_ml[w][row];
         if (saw_none(ml.x, ml.y)) continue;
         const float f = ex2_approx(ml.x - m);
-        const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + w * STAGES * S::STAGE) + row * D + dim);
+        const float *theirs = reinterpret_cast<const float *>(smem + w * STAGES * S::STAGE);
+        const float4 v = *reinterpret_cast<const float4 *>(theirs + row * D + dim);
         l = fmaf(f, ml.y, l);
         o.x = fmaf(f, v.x, o.x);
         o.y = fmaf(f, v.y, o.y);
@@ -996,7 +1004,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
         const bool none = saw_none(m, l);
         const float inv = none ? 0.f : 1.f / l;
         const int64_t at = out_row(p, d.x, d.y, d.z + row);
-        *reinterpret_cast<uint2 *>(p.o + at * D + dim) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        *reinterpret_cast<uint2 *>(p.o + at * D + dim) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         if (dim == 0) p.lse[at] = none ? -INFINITY : (m + log2f(l)) * kLn2;
       } else {
         *reinterpret_cast<float4 *>(p.ws_o + (part + row) * D + dim) = o;
@@ -1080,7 +1089,8 @@ __global__ void __launch_bounds__(kMergeThreads) attn_kv4_merge_kernel(const Kv4
           ml[u] = p.ws_ml[at];
 #pragma unroll
           for (int v = 0; v < V; ++v)
-            if (v * 128 + lane * 4 < D) w[u][v] = *reinterpret_cast<const float4 *>(p.ws_o + at * D + v * 128 + lane * 4);
+            if (v * 128 + lane * 4 < D)
+              w[u][v] = *reinterpret_cast<const float4 *>(p.ws_o + at * D + v * 128 + lane * 4);
         }
         float now = m;
 #pragma unroll

@@ -146,7 +146,8 @@ def attn_rope_table(rot_dim: int, sections=None, base: float = 10000.0, inv_freq
     if rot_dim % 2 or len(axis) != n or len(freq) != n:
         raise ValueError(f"rot_dim {rot_dim} needs {n} frequencies: sections have {len(axis)}, inv_freq {len(freq)}")
     host = torch.empty((n, 2), dtype=torch.int64)
-    rc = load_library().attn_rope_table((ctypes.c_double * n)(*freq), (ctypes.c_int * n)(*axis), n, max(axis, default=0) + 1,
+    rc = load_library().attn_rope_table((ctypes.c_double * n)(*freq), (ctypes.c_int * n)(*axis), n,
+                                        max(axis, default=0) + 1,
                                         host.data_ptr())
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_rope_table")
@@ -416,7 +417,8 @@ def attn_fwd_kv4(q, cu, lens, table, cache, page_size: int, scale: float | None 
         stride = _rows(table, index)
         B, width = table.shape
         if cu.shape != (B + 1,) or lens.shape != (B,):
-            raise ValueError(f"cu {tuple(cu.shape)} / lens {tuple(lens.shape)} do not match {B} requests (rows of table)")
+            raise ValueError(f"cu {tuple(cu.shape)} / lens {tuple(lens.shape)} do not match {B} requests "
+                             "(rows of table)")
         _dense(cu, "cu", _I32, (B + 1,), index)
         _dense(lens, "lens", _I32, (B,), index)
         _dense(out, "out", _BF16, (T, Hq, D), index)

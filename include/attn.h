@@ -463,6 +463,9 @@ ATTN_API int attn_kv4_read(const void *cache, int num_pages, const int *slots, v
  * scale  finite.  Products are exact on the codes (fp32 accumulation); the
  *        probabilities are rounded to 11 bits before the second product, O
  *        once to bf16.
+ * Made for few query rows (query tokens x Hq / Hkv up to about 64 a request).
+ * More work as well, at about 200 TFLOP/s; a long prompt chunk over a cached
+ * prefix is better served by attn_kv4_read and attn_fwd.
  * Nothing in a page past a request's last token, and nothing hidden from a
  * row, reaches that row's result, whatever it holds.  A table entry that is
  * not in 0 .. num_pages - 1, a length outside 0 .. max_pages * page_size, or
