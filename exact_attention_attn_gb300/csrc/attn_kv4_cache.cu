@@ -249,6 +249,7 @@ bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; 
 
 // The checks append and read share.
 int check_cache(const void *cache, int num_pages, int H, int D, int P, int T, const int *slots) {
+  if (T > 0x7fffffff - kTokens) return ATTN_ERR_ARG;  // a CTA's tokens are numbered past the last
   if (num_pages < 0 || T < 0 || H < 1 || H > 65535 || kv4_page_shift(P) < 0) return ATTN_ERR_ARG;
   if (D < 64 || D > ATTN_MAX_HEAD_DIM || D % 64 != 0) return ATTN_ERR_ARG;
   if ((int64_t)num_pages * P > 0x7fffffffLL) return ATTN_ERR_ARG;  // slots are 32-bit

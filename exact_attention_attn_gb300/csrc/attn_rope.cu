@@ -198,8 +198,10 @@ int attn_rope(const void *q, const long long *q_strides, void *q_out, const long
   if (rot < 16 || rot > D || rot % 16 != 0) return ATTN_ERR_ARG;
   if ((adjacent != 0 && adjacent != 1) || (backward != 0 && backward != 1)) return ATTN_ERR_ARG;
   if (pos_stride_axis < 0 || pos_stride_b < 0) return ATTN_ERR_ARG;
-  if ((int64_t)B * N * ((int64_t)Hq + Hkv) > (int64_t)1 << 40) return ATTN_ERR_ARG;
-  if (B == 0 || N == 0 || Hq + (int64_t)Hkv == 0) return ATTN_OK;
+  const int64_t heads = (int64_t)Hq + Hkv, tokens = (int64_t)B * N;
+  if (N > 0x7fffffff - 8) return ATTN_ERR_ARG;  // a CTA's tokens are numbered past the last
+  if (tokens == 0 || heads == 0) return ATTN_OK;
+  if (tokens > ((int64_t)1 << 40) / heads) return ATTN_ERR_ARG;
   if (!positions || !table) return ATTN_ERR_ARG;
   RopeParams p{};
   int rc;

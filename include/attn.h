@@ -337,7 +337,8 @@ ATTN_API int attn_fwd_fp8(const void *q8, const void *k8, const void *vt8, const
  * table  device pointer, rot / 2 entries of attn_rope_table made for at most
  *        `axes` axes (an entry of another axis is read as axis 0, and
  *        attn_fwd_status reports ATTN_ERR_DEVICE).
- * D      a multiple of 64 up to 1024; rot a multiple of 16, 16 .. D.
+ * D      a multiple of 64 up to 1024; rot a multiple of 16, 16 .. D.  N at most
+ *        2^31 - 9, B * N * (Hq + Hkv) at most 2^40.
  * All base addresses 16-byte aligned (positions: 4).  Asynchronous on
  * `stream`, one launch, no workspace; may be captured into a CUDA graph.
  *
@@ -430,9 +431,9 @@ ATTN_API int attn_pages_release(int *block_table, long long table_stride, int ma
  * attn_fwd_status reports ATTN_ERR_DEVICE.
  *
  * page_size is 16, 32 or 64; D a multiple of 64 up to 1024; num_pages *
- * page_size < 2^31.  Strides are element counts >= 0, multiples of 8; base
- * addresses 16-byte aligned (slots: 4).  Asynchronous on `stream`, one launch,
- * no workspace; may be captured into a CUDA graph.
+ * page_size < 2^31, T at most 2^31 - 33.  Strides are element counts >= 0, multiples
+ * of 8; base addresses 16-byte aligned (slots: 4).  Asynchronous on `stream`,
+ * one launch, no workspace; may be captured into a CUDA graph.
  */
 ATTN_API long long attn_kv4_page_bytes(int D, int page_size);
 ATTN_API int attn_kv4_append(const void *k, long long k_stride_t, long long k_stride_h, const void *v,

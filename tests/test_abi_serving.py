@@ -52,6 +52,23 @@ def test_rope_refusals(lib):  # noqa: F811
     assert rope(B=0, q=None) == 0 and rope(N=0, q=None) == 0 and rope(Hq=0, q=None) == 0
 
 
+def test_sizes_near_32_bits_are_refused(lib):  # noqa: F811
+    # a CTA's last tokens would have numbers past 2^31 - 1, and products of sizes pass 64 bits
+    p = Buf().p
+    s = strides(0, 0, 0)
+    most = 2 ** 31 - 1
+
+    def rope(B, N, Hq, Hk):
+        return lib.attn_rope(p, s, p, s, Hq, p, s, p, s, Hk, p, 0, 0, 1, p, B, N, 64, 64, 0, 0, None)
+
+    assert rope(1, most, 1, 0) == ARG and rope(1, most - 2, 1, 0) == ARG
+    assert rope(1 << 16, 1 << 17, most, 1) == ARG      # 2^64 + 2^33 rows
+    assert rope(most, most, most, most) == ARG
+    for T in (most, most - 30):
+        assert lib.attn_kv4_append(p, 0, 0, p, 0, 0, p, p, 4, T, 1, 64, 16, None) == ARG
+        assert lib.attn_kv4_read(p, 4, p, p, 0, 0, p, 0, 0, T, 1, 64, 16, None) == ARG
+
+
 def test_pages_refusals(lib):  # noqa: F811
     p = Buf().p
 
