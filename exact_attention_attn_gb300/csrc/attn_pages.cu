@@ -196,7 +196,8 @@ __global__ void __launch_bounds__(kMaxThreads) attn_pages_kernel(const PagesPara
       for (int u = 0; u < 4; ++u) slot[u] = from[u] ? *from[u] : -1;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (from[u]) slot[u] = slot[u] * p.P + (pos[u] & (p.P - 1));
+        if (from[u])  // -2: what the table or the stack holds has no 32-bit slot
+          slot[u] = (unsigned)slot[u] > (0x7fffffffu >> p.shift) ? -2 : slot[u] * p.P + (pos[u] & (p.P - 1));
       if (wide && i0 + 4 <= p.max_tokens) {
         *reinterpret_cast<int4 *>(p.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
         *reinterpret_cast<int4 *>(p.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);

@@ -388,9 +388,11 @@ ATTN_API int attn_rope(const void *q, const long long *q_strides, void *q_out, c
  * lens_out may be lens and free_count_out may be free_count (updates in
  * place); no other buffers may overlap.  page_size is 16, 32 or 64; B is 0 ..
  * ATTN_PAGES_MAX_REQUESTS; a row of the table has max_pages entries
- * (table_stride >= max_pages, max_pages * page_size < 2^31).  Page ids are not
- * interpreted.  One launch, no workspace, asynchronous on `stream`; may be
- * captured into a CUDA graph; deterministic.
+ * (table_stride >= max_pages, max_pages * page_size < 2^31).  Page ids are
+ * handed on as they are; a token whose page is not in 0 .. 2^31 / page_size - 1
+ * gets slot -2, which attn_kv4_append and attn_kv4_read report.  One launch, no
+ * workspace, asynchronous on `stream`; may be captured into a CUDA graph;
+ * deterministic.
  */
 #define ATTN_PAGES_MAX_REQUESTS 16384
 #define ATTN_PAGES_BAD_LENGTH 1

@@ -72,7 +72,8 @@ def pages_assign(table, lens, new, free, count, P, max_tokens):
             at -= 1
             table[r, -(-int(lens[r]) // P) + j] = free[at]
         for p in range(int(lens[r]), int(lens[r]) + int(new[r])):
-            slots[n], positions[n] = int(table[r, p // P]) * P + p % P, p
+            page = int(table[r, p // P])
+            slots[n], positions[n] = page * P + p % P if 0 <= page < 2 ** 31 // P else -2, p
             n += 1
         cu.append(n)
     return {"info": [0, n], "table": table, "lens": np.array(lens) + np.array(new), "free_count": at,

@@ -131,6 +131,20 @@ def test_empty_and_strided_table():
     assert wide.tolist() == [[8, 7, -5, -5] + [-5] * 5, [-5] * 9, [6, 5, 4, 3] + [-5] * 5]
 
 
+@pytest.mark.parametrize("P", [16, 64])
+def test_pages_without_a_slot(P):
+    # ids whose slots 32 bits do not hold, and ids below 0, on the stack and in the table
+    top = 2 ** 31 // P
+    table = np.array([[5, top, -1, -1, -1], [-1, -1, -1, -1, -1], [-7, -1, -1, -1, -1]])
+    free = np.array([3, -2 ** 31, top - 1, top, -1, 2 ** 31 - 1])
+    lens, new = np.array([P + 3, 0, 2]), np.array([2 * P, 3 * P, 5])
+    want = S.pages_assign(table, lens, new, free, 6, P, 6 * P)
+    assert want["info"][0] == 0 and set(want["slots"][want["slots"] < 0]) == {-2, -1}
+    dt = _dev(table)
+    got = attn_pages_assign(dt, _dev(lens), _dev(new), _dev(free), _dev([6]), P, 6 * P)
+    _same(got, want, dt, ("lens", "free_count", "cu", "slots", "positions"))
+
+
 def test_largest_batch():
     B, P = 16384, 16
     lens = np.zeros(B, dtype=np.int64)

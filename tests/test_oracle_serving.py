@@ -83,6 +83,14 @@ def test_pages_by_hand():
         assert bad["info"] == [bit, 0] and np.array_equal(bad["table"], table) and (bad["slots"] == -1).all()
 
 
+def test_pages_without_a_slot():
+    # page 2^27 of 16 tokens would have slot 2^31; -1 is no page
+    free = np.array([2 ** 27, -1, 2 ** 27 - 1])
+    got = S.pages_assign(np.full((1, 3), -1), [0], [33], free, 3, 16, 33)
+    assert got["info"] == [0, 33] and got["table"].tolist() == [[2 ** 27 - 1, -1, 2 ** 27]]
+    assert got["slots"].tolist() == list(range(2 ** 31 - 16, 2 ** 31)) + [-2] * 17
+
+
 def test_kv4_quantise():
     r = np.random.default_rng(5)
     x = S.to_bf16(r.standard_normal((7, 3, 192)) * np.exp(r.uniform(-3, 3, (7, 3, 192))))
