@@ -135,6 +135,11 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
   return (a | b) >> 31 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
+// The tiles of a request whose cu descends: it has no row, and no other request
+// has as many.  Where cu descends, requests could share query tokens and the line
+// of units be longer than the host took it to be, so the line is left empty.
+constexpr int kDescends = 1 << 30;
+
 // What a request's tiles look like, from the device arrays, with whatever
 // they hold brought into range (reported once through the status word).
 struct Request {
@@ -153,7 +158,7 @@ __device__ __forceinline__ Request load_request(const Kv4Params &p, int r) {
   q.nq = t1 - q.t0;
   q.len = min(max(l, 0), room);
   if (q.t0 != a || t1 != b || q.len != l) atomicCAS(p.status, 0, kStatusDevice);
-  q.tiles = max(1, (q.len + S::TK - 1) / S::TK);
+  q.tiles = b < a ? kDescends : max(1, (q.len + S::TK - 1) / S::TK);
   q.rt = (int)(((int64_t)q.nq * p.group + S::R - 1) / S::R);
   return q;
 }
@@ -279,9 +284,11 @@ __device__ __forceinline__ void find_piece_few(const Kv4Params &p, Piece &pc) {
     const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += u;
   }
-  set_piece<S>(p, __shfl_sync(0xffffffffu, inc, 31), __reduce_max_sync(0xffffffffu, longest), warp, pc);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  const bool empty = longest >= kDescends;
+  set_piece<S>(p, empty ? 0 : __shfl_sync(0xffffffffu, inc, 31), longest, warp, pc);
   Place mine_at{}, cta_at{};
-  int64_t a = inc - mine;
+  int64_t a = empty ? pc.cta_end + 1 : inc - mine;
   int each = 0;
   bool has = false, has_cta = false;
 #pragma unroll
@@ -342,6 +349,7 @@ __device__ __forceinline__ void find_piece(const Kv4Params &p, Piece &pc) {
     total += wsum[w];
     longest = max(longest, wmax[w]);
   }
+  if (longest >= kDescends) total = 0;
   set_piece<S>(p, total, longest, warp, pc);
   int64_t a = before + inc - mine;
   if (mine > 0 && a < pc.cta_end && a + mine > pc.cta_begin) {  // some of the thread's requests are here

@@ -473,7 +473,9 @@ ATTN_API int attn_kv4_read(const void *cache, int num_pages, const int *slots, v
  * row, reaches that row's result, whatever it holds.  A table entry that is
  * not in 0 .. num_pages - 1, a length outside 0 .. max_pages * page_size, or
  * query tokens outside 0 .. T is brought into range (that request's result is
- * then undefined) and attn_fwd_status reports ATTN_ERR_DEVICE.
+ * then undefined) and attn_fwd_status reports ATTN_ERR_DEVICE.  So it does
+ * where cu descends; the whole call's result is then undefined.  o and lse must
+ * not overlap each other or an input.
  *
  * q, o, lse and cache 16-byte aligned, q_stride_t and q_stride_h multiples of
  * 8 and >= 0; cu, lens and block_table 4-byte aligned.  (T * Hq / Hkv / 8 + B) *

@@ -351,6 +351,24 @@ def test_bad_metadata_is_reported_and_stays_in_range():
     assert attn_fwd_status() == 0
 
 
+@pytest.mark.parametrize("B", [3, 40, 300])
+def test_descending_cu_is_reported_and_costs_no_work(B):
+    # each other request would claim all the tokens: B / 2 times the work that the sizes allow
+    H, D, P, T = 2, 64, 16, 1024
+    cache = _random_cache(8, H, D, P, 4)
+    q = _randn((T, 4, D), 8)
+    dev = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    cu, lens = [T * (i & 1) for i in range(B + 1)], dev([128] * B)
+    table = dev([list(range(8))] * B)
+    out, lse = torch.full((T, 4, D), 5.0, dtype=torch.bfloat16, device="cuda"), torch.full((T, 4), 5.0, device="cuda")
+    attn_fwd_kv4(q, dev(cu), lens, table, cache, P, out=out, lse=lse)
+    assert attn_fwd_status() == -7
+    assert (out == 5).all() and (lse == 5).all()
+    cu = [0] * (B - 1) + [T, T]
+    attn_fwd_kv4(q, dev(cu), lens, table, cache, P, causal=False, out=out, lse=lse)
+    assert attn_fwd_status() == 0 and torch.isfinite(lse).all() and (lse[:, 0] != 5).any()
+
+
 def test_no_pages_and_no_tokens():
     H, D, P = 1, 64, 16
     q = _randn((2, 2, D), 1)
