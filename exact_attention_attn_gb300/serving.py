@@ -9,11 +9,13 @@ A decode or prefill step runs
     o, lse = attn_fwd_kv4(q, step["cu"], step["lens"], table, cache, page_size)
 
 without the host knowing a length.  Every function runs asynchronously on
-``stream`` (default: torch's current stream on the tensors' device); tensors
-that it allocates itself are kept from reuse until that stream has passed.
+``stream`` (default: torch's current stream on the tensors' device; a stream or
+its handle).  Tensors that a call allocates itself come from that stream's
+memory and are kept from reuse until the current stream has passed as well.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -47,18 +49,35 @@ def _sig(t):
     return t.dtype, t.get_device(), t.shape, t.stride()
 
 
-def _run(fn, what, index, stream, made, *args):
-    """fn(*args, stream) with the tensors' device current.  ``made``: tensors
-    allocated here for the current stream, which may be used on another one."""
+_default_memory = contextlib.nullcontext()
+
+
+def _memory(stream, index):
+    """Where tensors for a call on ``stream`` are allocated: a block of the
+    current stream's may still be in use there, ahead of the call."""
+    if stream is None:
+        return _default_memory
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=f"cuda:{index}")  # 1: the legacy default
+    return torch.cuda.stream(stream)
+
+
+def _keep_for_current(stream, index, *made):
+    """The caller uses tensors made for another stream on the current one."""
+    if stream is not None:
+        for t in made:
+            t.record_stream(torch.cuda.current_stream(index))
+
+
+def _run(fn, what, index, stream, *args):
+    """fn(*args, stream) with the tensors' device current."""
     if stream is None and index == torch.cuda.current_device():
         rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
             s = torch.cuda.current_stream() if stream is None else stream
             rc = fn(*args, s.cuda_stream if hasattr(s, "cuda_stream") else int(s))
-        if isinstance(stream, torch.cuda.Stream):
-            for t in made:
-                t.record_stream(stream)
     if rc != ATTN_OK:
         raise AttnError(rc, what)
 
@@ -187,16 +206,17 @@ def _rope_plan(q, k, positions, table, out_q, out_k):
 
 
 def _rope(q, k, positions, table, adjacent, out_q, out_k, backward, stream, what):
-    made = ()
     if out_q is None or (out_k is None and k is not None):
         _cuda(q, "q", _BF16, 4)
         made = []
-        if out_q is None:
-            out_q = torch.empty_like(q)
-            made.append(out_q)
-        if out_k is None and k is not None:
-            out_k = torch.empty_like(k)
-            made.append(out_k)
+        with _memory(stream, q.get_device()):
+            if out_q is None:
+                out_q = torch.empty_like(q)
+                made.append(out_q)
+            if out_k is None and k is not None:
+                out_k = torch.empty_like(k)
+                made.append(out_k)
+        _keep_for_current(stream, q.get_device(), *made)
     if k is None:
         if out_k is not None:
             raise ValueError("out_k without k")
@@ -209,7 +229,7 @@ def _rope(q, k, positions, table, adjacent, out_q, out_k, backward, stream, what
         kp = kop = None
     else:
         kp, kop = k.data_ptr(), out_k.data_ptr()
-    _run(load_library().attn_rope, what, index, stream, made, q.data_ptr(), qs, out_q.data_ptr(), qos, hq, kp, ks, kop, kos,
+    _run(load_library().attn_rope, what, index, stream, q.data_ptr(), qs, out_q.data_ptr(), qos, hq, kp, ks, kop, kos,
          hk, positions.data_ptr(), pa, pb, axes, table.data_ptr(), B, N, D, rot, 1 if adjacent else 0, backward)
     return out_q, out_k
 
@@ -230,23 +250,24 @@ def attn_rope_bwd(dq, dk, positions, table, adjacent: bool = False, out_q=None, 
 
 # ---------------------------------------------------------------- pages
 
-def _int_outs(like, want, out):
+def _int_outs(like, want, out, stream):
     """The int32 outputs by name (``want``: their lengths): given ones checked, the others made."""
-    got, made = {}, []
+    got, made, index = {}, [], like.get_device()
     if out:
-        index = like.get_device()
         for name in out:
             if name not in want:
                 raise ValueError(f"unknown output {name!r}")
-    for name, n in want.items():
-        t = out.get(name) if out else None
-        if t is None:
-            t = torch.empty(n, dtype=_I32, device=like.device)
-            made.append(t)
-        else:
-            _dense(t, name, _I32, (n,), index)
-        got[name] = t
-    return got, made
+    with _memory(stream, index):
+        for name, n in want.items():
+            t = out.get(name) if out else None
+            if t is None:
+                t = torch.empty(n, dtype=_I32, device=like.device)
+                made.append(t)
+            else:
+                _dense(t, name, _I32, (n,), index)
+            got[name] = t
+    _keep_for_current(stream, index, *made)
+    return got
 
 
 def _page_state(table, lens, arg, arg_name, free_pages, free_count):
@@ -279,15 +300,15 @@ def attn_pages_assign(table, lens, new_lens, free_pages, free_count, page_size: 
                *out, *map(_sig, out.values()))
         plan = _plans.get(key)
     if plan:
-        o, made = out, ()
+        o = out
     else:
         plan = _page_state(table, lens, new_lens, "new_lens", free_pages, free_count)
-        o, made = _int_outs(table, {"lens": plan[2], "free_count": 1, "cu": plan[2] + 1, "slots": max_tokens,
-                                    "positions": max_tokens, "info": 2}, out)
+        o = _int_outs(table, {"lens": plan[2], "free_count": 1, "cu": plan[2] + 1, "slots": max_tokens,
+                              "positions": max_tokens, "info": 2}, out, stream)
         if key:
             _keep(key, plan)
     stride, index, B, width, capacity = plan
-    _run(load_library().attn_pages_assign, "attn_pages_assign", index, stream, made, table.data_ptr(), stride, width,
+    _run(load_library().attn_pages_assign, "attn_pages_assign", index, stream, table.data_ptr(), stride, width,
          lens.data_ptr(), new_lens.data_ptr(), B, page_size, free_pages.data_ptr(), capacity, free_count.data_ptr(),
          o["lens"].data_ptr(), o["free_count"].data_ptr(), o["cu"].data_ptr(), o["slots"].data_ptr(),
          o["positions"].data_ptr(), max_tokens, o["info"].data_ptr())
@@ -300,8 +321,8 @@ def attn_pages_release(table, lens, keep_lens, free_pages, free_count, page_size
     place; returns a dict of lens [B], free_count [1] and info [2]."""
     stride, index, B, width, capacity = _page_state(table, lens, keep_lens, "keep_lens", free_pages, free_count)
     _written(free_pages.stride(), free_pages.shape, "free_pages")
-    o, made = _int_outs(table, {"lens": B, "free_count": 1, "info": 2}, out)
-    _run(load_library().attn_pages_release, "attn_pages_release", index, stream, made, table.data_ptr(), stride, width,
+    o = _int_outs(table, {"lens": B, "free_count": 1, "info": 2}, out, stream)
+    _run(load_library().attn_pages_release, "attn_pages_release", index, stream, table.data_ptr(), stride, width,
          lens.data_ptr(), keep_lens.data_ptr(), B, page_size, free_pages.data_ptr(), capacity, free_count.data_ptr(),
          o["lens"].data_ptr(), o["free_count"].data_ptr(), o["info"].data_ptr())
     return o
@@ -353,23 +374,24 @@ def attn_kv4_append(k, v, slots, cache, page_size: int, stream=None) -> None:
         ks, vs = _view(k, "k", (T, H, D), index), _view(v, "v", (T, H, D), index)
         plan = _keep(key, (index, *ks, *vs, pages, T, H, D))
     index, kt, kh, vt, vh, pages, T, H, D = plan
-    _run(load_library().attn_kv4_append, "attn_kv4_append", index, stream, (), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+    _run(load_library().attn_kv4_append, "attn_kv4_append", index, stream, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
          slots.data_ptr(), cache.data_ptr(), pages, T, H, D, page_size)
 
 
 def attn_kv4_read(slots, cache, page_size: int, out_k=None, out_v=None, stream=None):
     """K and V of the slots (int32 [T]) as bf16 [Hkv, T, D]: k[None], v[None]
     are attn_fwd's operands for a cached prefix.  Slot -1 reads as zeros."""
-    made = ()
     if out_k is None or out_v is None:
-        _, _, H, D = _cache(cache, page_size)
+        index, _, H, D = _cache(cache, page_size)
         made = []
-        if out_k is None:
-            out_k = torch.empty((H, slots.shape[0], D), dtype=_BF16, device=cache.device)
-            made.append(out_k)
-        if out_v is None:
-            out_v = torch.empty((H, slots.shape[0], D), dtype=_BF16, device=cache.device)
-            made.append(out_v)
+        with _memory(stream, index):
+            if out_k is None:
+                out_k = torch.empty((H, slots.numel(), D), dtype=_BF16, device=cache.device)
+                made.append(out_k)
+            if out_v is None:
+                out_v = torch.empty((H, slots.numel(), D), dtype=_BF16, device=cache.device)
+                made.append(out_v)
+        _keep_for_current(stream, index, *made)
     key = ("read", page_size, _sig(slots), _sig(cache), _sig(out_k), _sig(out_v))
     plan = _plans.get(key)
     if plan is None:
@@ -381,7 +403,7 @@ def attn_kv4_read(slots, cache, page_size: int, out_k=None, out_v=None, stream=N
         _written(vs, out_v.shape, "out_v")
         plan = _keep(key, (index, *ks, *vs, pages, T, H, D))
     index, kh, kt, vh, vt, pages, T, H, D = plan
-    _run(load_library().attn_kv4_read, "attn_kv4_read", index, stream, made, cache.data_ptr(), pages, slots.data_ptr(),
+    _run(load_library().attn_kv4_read, "attn_kv4_read", index, stream, cache.data_ptr(), pages, slots.data_ptr(),
          out_k.data_ptr(), kh, kt, out_v.data_ptr(), vh, vt, T, H, D, page_size)
     return out_k, out_v
 
@@ -396,16 +418,19 @@ def attn_fwd_kv4(q, cu, lens, table, cache, page_size: int, scale: float | None 
     and lens[r] cached tokens, theirs among them (``causal``: bottom-right
     aligned, as attn_fwd).  Rows outside cu[0] .. cu[B] are left as they were.
     Head dims 64, 128, 192, 256."""
-    made = ()
     if out is None or lse is None:
-        _view(q, "q", q.shape, cache.get_device())
+        index = cache.get_device()
+        if stream is not None:
+            _cuda(q, "q", _BF16, 3, index)
         made = []
-        if out is None:
-            out = torch.empty(q.shape, dtype=_BF16, device=q.device)
-            made.append(out)
-        if lse is None:
-            lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
-            made.append(lse)
+        with _memory(stream, index):
+            if out is None:
+                out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+                made.append(out)
+            if lse is None:
+                lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
+                made.append(lse)
+        _keep_for_current(stream, index, *made)
     key = ("fwd", page_size, _sig(q), _sig(cu), _sig(lens), _sig(table), _sig(cache), _sig(out), _sig(lse))
     plan = _plans.get(key)
     if plan is None:
@@ -425,7 +450,7 @@ def attn_fwd_kv4(q, cu, lens, table, cache, page_size: int, scale: float | None 
         _dense(lse, "lse", _F32, (T, Hq), index)
         plan = _keep(key, (index, *qs, stride, width, pages, B, T, Hq, H, D, 1.0 / math.sqrt(D)))
     index, qt, qh, stride, width, pages, B, T, Hq, H, D, usual = plan
-    _run(load_library().attn_fwd_kv4, "attn_fwd_kv4", index, stream, made, q.data_ptr(), qt, qh, cu.data_ptr(),
+    _run(load_library().attn_fwd_kv4, "attn_fwd_kv4", index, stream, q.data_ptr(), qt, qh, cu.data_ptr(),
          lens.data_ptr(), table.data_ptr(), stride, width, cache.data_ptr(), pages, out.data_ptr(), lse.data_ptr(), B, T,
          Hq, H, D, page_size, usual if scale is None else scale, 1 if causal else 0)
     return out, lse

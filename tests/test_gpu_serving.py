@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from exact_attention_attn_gb300 import (attn_fwd_kv4, attn_fwd_status, attn_kv4_append, attn_kv4_cache,
+from exact_attention_attn_gb300 import (attn_fwd_kv4, attn_fwd_status, attn_kv4_append, attn_kv4_cache, attn_kv4_read,
                                         attn_pages_assign, attn_pages_release, attn_rope, attn_rope_axes,
                                         attn_rope_table)
 from exact_attention_attn_gb300.workloads import to_f64
@@ -188,6 +188,33 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         a.check()
         b.check()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_for_another_stream_take_no_block_in_use(handle):
+    # a block whose last reader still waits on the current stream is not given to a call on another stream
+    s = Server(4, 100, 300, 60, seed=37)
+    s.load([40, 3, 5, 9])
+    s.step()
+    s.check()
+    q4, slots, pos = s.q.transpose(0, 1)[None], s.out["slots"], s.out["positions"][None, None].expand(3, 1, s.T)
+    table, side = s.table.clone(), torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    calls = {
+        s.q.numel() * 2: lambda: attn_fwd_kv4(s.q, s.out["cu"], s.lens, s.table, s.cache, P, stream=stream),
+        s.q.numel() * 2 + 1: lambda: attn_rope(q4, None, pos, s.rope, stream=stream),
+        s.k.numel() * 2: lambda: attn_kv4_read(slots, s.cache, P, stream=stream),
+        s.T * 4: lambda: attn_pages_assign(table, s.lens, s.new, s.free, s.count, P, s.T, stream=stream)}
+    for size, call in calls.items():
+        used = [torch.full((size,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(40_000_000)  # some 20 ms
+        kept = [u.clone() for u in used]
+        del used
+        out = call()
+        torch.cuda.synchronize()
+        assert all((k == 7).all() for k in kept), size
+        del out
 
 
 def test_outputs_are_kept_for_the_other_stream():
