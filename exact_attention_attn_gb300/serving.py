@@ -103,6 +103,12 @@ def _dense(t, name, dtype, shape, index):
     raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
+def _sizes(*sizes):
+    """The library's sizes are C ints; ctypes would pass the low half of a larger one."""
+    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
+        raise ValueError(f"sizes {sizes} pass 32 bits")
+
+
 def _last_dim(t, name):
     """The strides before the last dim, in elements (0 for a dim of size one: it is never stepped along)."""
     s = t.stride()
@@ -184,7 +190,7 @@ def _rope_plan(q, k, positions, table, out_q, out_k):
         raise ValueError(f"positions {tuple(positions.shape)} do not match [axes, {B}, {N}]")
     if N > 1 and ps[2] != 1:
         raise ValueError("positions' last dim must be contiguous")
-    half = table.shape[0]
+    half = table.shape[0] if table.dim() else 0
     _dense(table, "table", _I64, (half, 2), index)
     heads, strides = [], []
     for x, out, name in ((q, out_q, "q"), (k, out_k, "k")):
@@ -202,6 +208,7 @@ def _rope_plan(q, k, positions, table, out_q, out_k):
         _written(so, out.shape, "out_" + name)
         heads.append(x.shape[1])
         strides += [_Strides(*_last_dim(x, name)), _Strides(*so)]
+    _sizes(*heads, axes, B, N, D, 2 * half)
     return (index, heads[0], heads[1], *strides, ps[0] if axes > 1 else 0, ps[1] if B > 1 else 0, axes, B, N, D, 2 * half)
 
 
@@ -270,16 +277,17 @@ def _int_outs(like, want, out, stream):
     return got
 
 
-def _page_state(table, lens, arg, arg_name, free_pages, free_count):
+def _page_state(table, lens, arg, arg_name, free_pages, free_count, page_size, max_tokens=0):
     index = table.get_device()
     stride = _rows(table, None)
     B, width = table.shape
     _written(table.stride(), table.shape, "table")
     _dense(lens, "lens", _I32, (B,), index)
     _dense(arg, arg_name, _I32, (B,), index)
-    capacity = free_pages.shape[0]
+    capacity = free_pages.numel()
     _dense(free_pages, "free_pages", _I32, (capacity,), index)
     _dense(free_count, "free_count", _I32, (1,), index)
+    _sizes(B, width, capacity, page_size, max_tokens)
     return stride, index, B, width, capacity
 
 
@@ -296,13 +304,13 @@ def attn_pages_assign(table, lens, new_lens, free_pages, free_count, page_size: 
     out["free_count"] free_count, for updates in place."""
     key = plan = None
     if out and len(out) == 6:
-        key = ("assign", max_tokens, _sig(table), _sig(lens), _sig(new_lens), _sig(free_pages), _sig(free_count),
+        key = ("assign", page_size, max_tokens, _sig(table), _sig(lens), _sig(new_lens), _sig(free_pages), _sig(free_count),
                *out, *map(_sig, out.values()))
         plan = _plans.get(key)
     if plan:
         o = out
     else:
-        plan = _page_state(table, lens, new_lens, "new_lens", free_pages, free_count)
+        plan = _page_state(table, lens, new_lens, "new_lens", free_pages, free_count, page_size, max_tokens)
         o = _int_outs(table, {"lens": plan[2], "free_count": 1, "cu": plan[2] + 1, "slots": max_tokens,
                               "positions": max_tokens, "info": 2}, out, stream)
         if key:
@@ -319,7 +327,8 @@ def attn_pages_release(table, lens, keep_lens, free_pages, free_count, page_size
     """Requests cut to ``keep_lens`` tokens (0: finished; negative: left alone),
     their pages back on the stack.  ``table`` and ``free_pages`` are updated in
     place; returns a dict of lens [B], free_count [1] and info [2]."""
-    stride, index, B, width, capacity = _page_state(table, lens, keep_lens, "keep_lens", free_pages, free_count)
+    stride, index, B, width, capacity = _page_state(table, lens, keep_lens, "keep_lens", free_pages, free_count,
+                                                        page_size)
     _written(free_pages.stride(), free_pages.shape, "free_pages")
     o = _int_outs(table, {"lens": B, "free_count": 1, "info": 2}, out, stream)
     _run(load_library().attn_pages_release, "attn_pages_release", index, stream, table.data_ptr(), stride, width,
@@ -369,9 +378,10 @@ def attn_kv4_append(k, v, slots, cache, page_size: int, stream=None) -> None:
     plan = _plans.get(key)
     if plan is None:
         index, pages, H, D = _cache(cache, page_size)
-        T = slots.shape[0]
+        T = slots.numel()
         _dense(slots, "slots", _I32, (T,), index)
         ks, vs = _view(k, "k", (T, H, D), index), _view(v, "v", (T, H, D), index)
+        _sizes(pages, T, H, D)
         plan = _keep(key, (index, *ks, *vs, pages, T, H, D))
     index, kt, kh, vt, vh, pages, T, H, D = plan
     _run(load_library().attn_kv4_append, "attn_kv4_append", index, stream, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
@@ -396,11 +406,12 @@ def attn_kv4_read(slots, cache, page_size: int, out_k=None, out_v=None, stream=N
     plan = _plans.get(key)
     if plan is None:
         index, pages, H, D = _cache(cache, page_size)
-        T = slots.shape[0]
+        T = slots.numel()
         _dense(slots, "slots", _I32, (T,), index)
         ks, vs = _view(out_k, "out_k", (H, T, D), index), _view(out_v, "out_v", (H, T, D), index)
         _written(ks, out_k.shape, "out_k")
         _written(vs, out_v.shape, "out_v")
+        _sizes(pages, T, H, D)
         plan = _keep(key, (index, *ks, *vs, pages, T, H, D))
     index, kh, kt, vh, vt, pages, T, H, D = plan
     _run(load_library().attn_kv4_read, "attn_kv4_read", index, stream, cache.data_ptr(), pages, slots.data_ptr(),
@@ -435,8 +446,9 @@ def attn_fwd_kv4(q, cu, lens, table, cache, page_size: int, scale: float | None 
     plan = _plans.get(key)
     if plan is None:
         index, pages, H, D = _cache(cache, page_size)
-        T, Hq = q.shape[0], q.shape[1]
-        if q.dim() == 3 and q.shape[2] != D:
+        _cuda(q, "q", _BF16, 3, index)
+        T, Hq = q.shape[:2]
+        if q.shape[2] != D:
             raise ValueError(f"q {tuple(q.shape)} does not match the cache's head dim {D}")
         qs = _view(q, "q", (T, Hq, D), index)
         stride = _rows(table, index)
@@ -448,6 +460,7 @@ def attn_fwd_kv4(q, cu, lens, table, cache, page_size: int, scale: float | None 
         _dense(lens, "lens", _I32, (B,), index)
         _dense(out, "out", _BF16, (T, Hq, D), index)
         _dense(lse, "lse", _F32, (T, Hq), index)
+        _sizes(width, pages, B, T, Hq, H, D)
         plan = _keep(key, (index, *qs, stride, width, pages, B, T, Hq, H, D, 1.0 / math.sqrt(D)))
     index, qt, qh, stride, width, pages, B, T, Hq, H, D, usual = plan
     _run(load_library().attn_fwd_kv4, "attn_fwd_kv4", index, stream, q.data_ptr(), qt, qh, cu.data_ptr(),

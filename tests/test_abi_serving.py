@@ -125,6 +125,51 @@ def test_kv4_refusals(lib):  # noqa: F811
     assert fwd(B=0, q=None) == 0 and fwd(T=0, q=None) == 0
 
 
+def test_binding_refuses_sizes_past_32_bits(lib, monkeypatch):  # noqa: F811
+    # a size that 32 bits do not hold must not reach the library as its low half (meta tensors: no memory behind them)
+    import exact_attention_attn_gb300 as A
+    from exact_attention_attn_gb300 import serving
+    monkeypatch.setattr(serving, "_cuda", lambda *a: None)
+    monkeypatch.setattr(serving, "_dense", lambda *a: None)
+    monkeypatch.setattr(serving, "_run", lambda *a: pytest.fail("called"))
+    bf, i32, big = torch.bfloat16, torch.int32, 2 ** 32 + 1
+    one, many = torch.zeros(1, dtype=i32), torch.empty(big, dtype=i32, device="meta")
+    cache, table = A.attn_kv4_cache(2, 1, 64, 16, device="cpu"), A.attn_rope_table(64, device="cpu")
+    x = torch.empty((big, 1, 64), dtype=bf, device="meta")
+    y = x.transpose(0, 1)
+    with pytest.raises(ValueError, match="32 bits"):
+        A.attn_kv4_append(x, x, many, cache, 16)
+    with pytest.raises(ValueError, match="32 bits"):
+        A.attn_kv4_read(many, cache, 16, out_k=y, out_v=y)
+    with pytest.raises(ValueError, match="32 bits"):
+        A.attn_fwd_kv4(x, one.expand(2), one, one[None], cache, 16, out=x, lse=one)
+    with pytest.raises(ValueError, match="32 bits"):
+        A.attn_rope(y[None], None, many[None, None], table, out_q=y[None])
+    for call in (lambda: A.attn_pages_assign(one[None], one, one, many, one, 16, 4),
+                 lambda: A.attn_pages_assign(one[None], one, one, one, one, 2 ** 32 + 16, 4),
+                 lambda: A.attn_pages_assign(one[None], one, one, one, one, 16, big),
+                 lambda: A.attn_pages_assign(many[None], one, one, one, one, 16, 4),
+                 lambda: A.attn_pages_release(one[None], one, one, many, one, 16),
+                 lambda: A.attn_pages_release(one[None], one, one, one, one, 2 ** 32 + 16)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+
+
+def test_binding_refuses_other_ranks(lib):  # noqa: F811
+    import exact_attention_attn_gb300 as A
+    cache, one = A.attn_kv4_cache(2, 1, 64, 16, device="cpu"), torch.zeros(1, dtype=torch.int32)
+    x, scalar = torch.zeros(1, 1, 64, dtype=torch.bfloat16), torch.zeros((), dtype=torch.int32)
+    for call in (lambda: A.attn_kv4_append(x, x, scalar, cache, 16), lambda: A.attn_kv4_read(scalar, cache, 16),
+                 lambda: A.attn_fwd_kv4(x[0, 0], one, one, one[None], cache, 16),
+                 lambda: A.attn_fwd_kv4(x[0], one, one, one[None], cache, 16),
+                 lambda: A.attn_fwd_kv4(x, scalar, one, one, cache, 16),
+                 lambda: A.attn_pages_assign(one[None], one, one, scalar, one, 16, 4),
+                 lambda: A.attn_pages_release(one, one, one, one, one, 16),
+                 lambda: A.attn_rope(x[None], None, one[None, None], scalar)):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_binding_refuses_cpu_tensors_and_shapes(lib):  # noqa: F811
     import exact_attention_attn_gb300 as A
     bf, i32 = torch.bfloat16, torch.int32
