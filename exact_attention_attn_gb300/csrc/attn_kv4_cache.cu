@@ -10,10 +10,11 @@
 //
 // The differences are formed on x / 16, so that max - min of finite values
 // stays finite; the factor is a power of two and leaves every result alone.
-// The quotient is rounded as a division would round it, from one reciprocal
-// of the group's scale and a residual (q0 = d r, q = q0 + (d - q0 s) r), three
-// operations instead of a division's ten; groups whose scale is so small or
-// large that these could leave the normal range divide.
+// The quotient comes from one reciprocal of the group's scale, corrected by its
+// exact residual (q0 = d r, q = q0 + (d - q0 s) r: Markstein's correction, IBM
+// J. Res. Dev. 34, 1990), three operations instead of a division's ten; groups
+// whose scale is so small or large that these could leave the normal range
+// divide.
 //
 // Eight threads share a group (16 bytes of bfloat16 each, one 4-byte word of
 // codes); 32 consecutive tokens share a CTA, so that a warp writes four

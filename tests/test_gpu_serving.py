@@ -190,6 +190,39 @@ def test_two_streams_at_once():
         b.check()
 
 
+def test_two_threads_at_once():
+    import threading
+    servers = [Server(4, 100, 300, 60, seed=110), Server(4, 100, 300, 60, seed=130)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in servers:
+        s.load([40, 3, 5, 9])
+    torch.cuda.synchronize()
+    failed, ready = [], threading.Barrier(2)
+
+    def run(s, stream):
+        try:
+            with torch.cuda.stream(stream):
+                ready.wait(30)
+                s.step()
+                o, lse = s.o.clone(), s.lse.clone()
+                n = s.want["info"][1]
+                for _ in range(30):  # the same attention again, with outputs of its own
+                    a, b = attn_fwd_kv4(s.q, s.out["cu"], s.lens, s.table, s.cache, P)
+                    if not (torch.equal(a[:n], o[:n]) and torch.equal(b[:n], lse[:n])):
+                        failed.append("differs")
+        except Exception as e:  # noqa: BLE001
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=run, args=a) for a in zip(servers, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for s in servers:
+        s.check()
+
+
 @pytest.mark.parametrize("handle", [False, True])
 def test_outputs_for_another_stream_take_no_block_in_use(handle):
     # a block whose last reader still waits on the current stream is not given to a call on another stream
