@@ -29,8 +29,8 @@ _BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch
 # usual form is recognised with a handful of attribute reads, and only another form goes through the checks that say
 # what is wrong with it (or that it is fine).
 #
-# "Plans": what a call passes on besides its pointers (sizes, strides) depends on its tensors' types, shapes, strides and
-# devices alone.  It is checked and laid out once for each such signature and looked up afterwards.
+# "Plans": what a call passes on besides its pointers (sizes, strides) depends on its tensors' types, shapes, strides
+# and devices alone.  It is checked and laid out once for each such signature and looked up afterwards.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _Strides = ctypes.c_longlong * 3
@@ -59,7 +59,8 @@ def _memory(stream, index):
         return _default_memory
     if not isinstance(stream, torch.cuda.Stream):
         handle = int(getattr(stream, "cuda_stream", stream))
-        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=f"cuda:{index}")  # 1: the legacy default
+        handle = 0 if handle == 1 else handle  # two names of the legacy default stream
+        stream = torch.cuda.ExternalStream(handle, device=f"cuda:{index}")
     return torch.cuda.stream(stream)
 
 
@@ -209,7 +210,8 @@ def _rope_plan(q, k, positions, table, out_q, out_k):
         heads.append(x.shape[1])
         strides += [_Strides(*_last_dim(x, name)), _Strides(*so)]
     _sizes(*heads, axes, B, N, D, 2 * half)
-    return (index, heads[0], heads[1], *strides, ps[0] if axes > 1 else 0, ps[1] if B > 1 else 0, axes, B, N, D, 2 * half)
+    return (index, heads[0], heads[1], *strides, ps[0] if axes > 1 else 0, ps[1] if B > 1 else 0, axes, B, N, D,
+            2 * half)
 
 
 def _rope(q, k, positions, table, adjacent, out_q, out_k, backward, stream, what):
@@ -304,8 +306,8 @@ def attn_pages_assign(table, lens, new_lens, free_pages, free_count, page_size: 
     out["free_count"] free_count, for updates in place."""
     key = plan = None
     if out and len(out) == 6:
-        key = ("assign", page_size, max_tokens, _sig(table), _sig(lens), _sig(new_lens), _sig(free_pages), _sig(free_count),
-               *out, *map(_sig, out.values()))
+        key = ("assign", page_size, max_tokens, _sig(table), _sig(lens), _sig(new_lens), _sig(free_pages),
+               _sig(free_count), *out, *map(_sig, out.values()))
         plan = _plans.get(key)
     if plan:
         o = out
