@@ -1,7 +1,8 @@
 // The 4-bit KV cache: quantising tokens into their slots, and reading slots
 // back as bfloat16.
 //
-// Per token, kv head and 64 dims:  m = min x,  s = bf16((max x - m) / 15),
+// Per token, kv head and 64 dims:  m = min x,  s = (max x - m) / 15 as bfloat16
+// (of the float32 product ((max x - m) / 16) (16 / 15)),
 // c = rint((x - m) / s) in 0 .. 15 (0 where s = 0); the cache holds c in four
 // bits and (s, m) as bfloat16.  m is one of the bfloat16 inputs, so it is
 // held exactly; s is rounded to nearest once.  A group that holds an infinity
@@ -48,14 +49,6 @@ struct AppendParams {
   int *status;
 };
 
-// a / b rounded to nearest, from r = 1 / b to a few units in its last place: the
-// residual a - q0 b is exact, so its correction leaves an error far below the
-// last place of the quotient (and none where the quotient is a short number).
-__device__ __forceinline__ float quotient(float a, float b, float r) {
-  const float q0 = a * r;
-  return fmaf(fmaf(-q0, b, a), r, q0);
-}
-
 // Codes and pair of one group of 64 values, 8 of them (w) in each of 8 lanes.
 __device__ __forceinline__ void quantise8(const uint4 &w, uint32_t &codes, uint32_t &pair) {
   const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
@@ -77,9 +70,10 @@ __device__ __forceinline__ void quantise8(const uint4 &w, uint32_t &codes, uint3
     r = __hmin2_nan(r, t);
   }
   const float lo = __low2float(r) * 0.0625f, hi = -__high2float(r) * 0.0625f;
-  // s = bf16(((max - min) / 16) / (15 / 16))
+  // ((max - min) / 16) / (15 / 16), by the reciprocal: one product, whose rounding also decides where the value is
+  // halfway between two bfloat16 numbers
   const float d = hi - lo;
-  const __nv_bfloat16 sb = __float2bfloat16_rn(quotient(d, 0.9375f, 1.f / 0.9375f));
+  const __nv_bfloat16 sb = __float2bfloat16_rn(__fmul_rn(d, 1.f / 0.9375f));
   const float s = __bfloat162float(sb) * 0.0625f;
   uint16_t sbits, mbits;
   memcpy(&sbits, &sb, 2);
@@ -102,7 +96,10 @@ __device__ __forceinline__ void quantise8(const uint4 &w, uint32_t &codes, uint3
     }
     return;
   }
-  // two values per packed operation; the quotient is at most 15 (1 + 2^-8), so no code passes 15
+  // Two values per packed operation.  With inv = 1 / s to a few units in its last
+  // place, the residual e - q0 s is exact, so its correction leaves an error far
+  // below the last place of the quotient (and none where the quotient is a short
+  // number).  The quotient is at most 15 (1 + 2^-8), so no code passes 15.
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
   const uint64_t k16 = ptx::f2_pack(0.0625f, 0.0625f), nlo = ptx::f2_pack(-lo, -lo), ns = ptx::f2_pack(-s, -s);

@@ -418,7 +418,8 @@ ATTN_API int attn_pages_release(int *block_table, long long table_stride, int ma
  * pairs.  Per token, kv head and 64 dims:
  *     m = min x,  s = bf16((max x - m) / 15),  c = rint((x - m) / s) in 0..15
  * (c = 0 where s = 0), and the code stands for s c + m.  Rounding is to
- * nearest, ties to even.  A group that holds an infinity or a NaN gets s = m =
+ * nearest, ties to even; the quotient that s rounds is the float32 product
+ * fl(fl(max x / 16 - m / 16) * fl(16 / 15)).  A group that holds an infinity or a NaN gets s = m =
  * NaN and codes 0.
  *
  * attn_kv4_append writes token t's K and V into slot slots[t] = page *

@@ -108,7 +108,11 @@ def kv4_quantise(x):
     x = np.asarray(x, dtype=np.float64)
     y = x.reshape(x.shape[:-1] + (x.shape[-1] // GROUP, GROUP))
     m, hi = y.min(-1), y.max(-1)
-    s = to_bf16((hi - m) / 15)
+    # in float32, by the reciprocal: where (max - m) / 15 lies halfway between two
+    # bfloat16 numbers, the product's rounding decides
+    f = np.float32
+    with np.errstate(over="ignore", invalid="ignore"):
+        s = to_bf16(((hi.astype(f) * f(0.0625) - m.astype(f) * f(0.0625)) * (f(1) / f(0.9375))).astype(np.float64))
     q = np.where(s[..., None] > 0, (y - m[..., None]) / np.where(s > 0, s, 1.0)[..., None], 0.0)
     codes = np.clip(np.round(q), 0, 15).astype(np.int64)
     return codes.reshape(x.shape), s, m, q.reshape(x.shape)

@@ -130,6 +130,24 @@ def test_special_groups():
     assert torch.equal(ok[0, 1, :64].cpu(), x[1, 0, :64]) and torch.isnan(ok[0, 2, :64]).all() and (ok[0, 0] == 3).all()
 
 
+def test_scales_halfway_between_two_numbers():
+    # groups with one large value: their (max - min) / 15 often lies halfway between two bfloat16 numbers
+    T, H, D, P = 4096, 2, 64, 16
+    g = torch.Generator().manual_seed(11)
+    x = torch.rand((T, H, D), generator=g) * 2 - 1
+    x[..., 0] = 1 + 3 * torch.rand((T, H), generator=g)
+    x[..., 1] = -(32 + 40 * torch.rand((T, H), generator=g))
+    x = torch.where(torch.rand((T, H, 1), generator=g) < 0.5, x, -x).to(torch.bfloat16)
+    span = (x.double().amax(-1) - x.double().amin(-1)) / 15
+    low = torch.tensor(S.to_bf16(span.numpy() * (1 - 2.0 ** -20)))
+    high = torch.tensor(S.to_bf16(span.numpy() * (1 + 2.0 ** -20)))
+    assert ((low + high) / 2 == span)[low != high].sum() > 20  # the inputs hold such groups
+    cache, slots = attn_kv4_cache(T // P, H, D, P), np.arange(T)
+    attn_kv4_append(x.cuda(), (-x).cuda(), torch.tensor(slots, dtype=torch.int32, device="cuda"), cache, P)
+    _check_codes(x.double().numpy(), slots, cache, D, P, 0)
+    _check_codes(-x.double().numpy(), slots, cache, D, P, 1)
+
+
 def test_bad_slots_are_skipped_and_reported():
     T, H, D, P = 6, 2, 64, 16
     k = _randn((T, H, D), 1)

@@ -105,6 +105,12 @@ def test_kv4_quantise():
     line = np.tile(np.arange(16.0) * 0.25 - 1, 4)
     c, s, m, _ = S.kv4_quantise(line)
     assert s == 0.25 and m == -1 and np.array_equal(S.kv4_values(c, s, m), line)
+    # (max - m) / 15 = 2.2890625 and 2.4140625, halfway between two bfloat16 numbers
+    for hi, lo, want in ((1.8359375, -32.5, 2.296875), (34.25, -1.9609375, 2.421875)):
+        x = np.full(64, lo)
+        x[3] = hi
+        c, s, m, q = S.kv4_quantise(x)
+        assert s == want and m == lo and c[3] == 15 and c[4] == 0 and q[3] == (hi - lo) / want
     c, s, m, _ = S.kv4_quantise(np.full(64, 3.5))
     assert s == 0 and (c == 0).all() and m == 3.5
 
