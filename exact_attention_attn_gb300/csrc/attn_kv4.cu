@@ -45,8 +45,10 @@
 // first's end -- merges in the order of the tokens.  Where one item covers all
 // the pieces of a CTA its warps' parts are merged in shared memory first.
 // Where the items are few and short by the sizes alone (no more than SMs, at
-// most 4 tiles a warp), each is one CTA's and there is no second kernel: one
-// request of 129 tokens 6.4 us against 9.8, 8 requests of 1024 11.1 against 14.8.
+// most 8 tiles a warp), each has a cluster of 1 to 8 CTAs, whose parts are merged
+// through distributed shared memory, and there is no workspace and no second
+// kernel: one request of 129 tokens 6.4 us against 9.8, 8 requests of 1000 9.9
+// against 14.2, 4 of 4000 12.8 against 16.4.
 //
 // Memory.  Each warp owns a ring of stages of one tile (whole pages, 16 bytes
 // a lane and copy), and asks for the next tile as soon as a stage is read.
@@ -76,6 +78,8 @@ using namespace ptx;
 
 constexpr int kMostParts = 64;    // CTAs that one item is cut into, at most
 constexpr int kLeastUnits = 2;    // units of a piece, at least
+constexpr int kClusterSizes = 3;  // clusters of 2, 4 and 8 CTAs
+constexpr int kMostCluster = 1 << kClusterSizes;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoRef = -1e37f;  // reference of a row that has seen no key
@@ -91,7 +95,8 @@ struct Kv4Params {
   const uint8_t *cache;
   int num_pages, max_pages, B, T, H, group, shift, causal;
   float scale_log2;  // scale * log2 e
-  int pieces;        // warps of the grid; 0: a CTA for each item, no item is cut
+  int pieces;        // warps of the grid; 0: a cluster of CTAs for each item, no item is cut
+  int cluster;       // CTAs of a cluster
   float *ws_o;       // partial O of cut items: [pieces][2][R][D]
   float2 *ws_ml;     // their reference and l: [pieces][2][R]
   int4 *ws_cut;      // [pieces][2]: the item that each piece leaves unfinished
@@ -127,7 +132,7 @@ struct Shape {
     return P == 16 ? i * PAGE_BYTES + j * P * kKv4PairBytes : (j * P + i * 16) * kKv4PairBytes;
   }
   static_assert(STAGES >= 2, "a warp reads one stage while another fills");
-  static_assert(STAGES * STAGE >= R * D * 4, "a warp's part of a shared item fits its ring");
+  static_assert(STAGES * STAGE >= 2 * R * D * 4, "a warp's part of a shared item, and the CTA's, fit its ring");
 };
 
 // a / b for a >= 0, b > 0; in 32 bits where both fit, a third of the operations.
@@ -183,19 +188,21 @@ struct Piece {
   }
 };
 
-// One CTA for each item (few and short ones: spreading them further would cost
-// more in merging than it saves): the warps share the item's tiles, and its
-// parts are merged in shared memory, without a workspace or a second kernel.
+// One cluster of CTAs for each item (few and short ones: spreading them further
+// would cost more in merging than it saves): the cluster's warps share the item's
+// tiles, and its parts are merged in shared memory, without a workspace or a
+// second kernel.
 template <typename S>
 __device__ __forceinline__ void find_item(const Kv4Params &p, Piece &pc) {
   __shared__ Place found;
   __shared__ int tiles;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int item = (int)blockIdx.x / p.cluster, rank = (int)blockIdx.x % p.cluster;
   if (tid == 0) tiles = 0;
   __syncthreads();
   if (warp == 0) {  // items before each request, 32 requests at a time
     int64_t before = 0;
-    for (int base = 0; base < p.B && before <= blockIdx.x; base += 32) {
+    for (int base = 0; base < p.B && before <= item; base += 32) {
       Request q{};
       if (base + lane < p.B) q = load_request<S>(p, base + lane);
       const int64_t n = (int64_t)p.H * q.rt;
@@ -205,7 +212,7 @@ __device__ __forceinline__ void find_item(const Kv4Params &p, Piece &pc) {
         const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += u;
       }
-      const int64_t i = (int64_t)blockIdx.x - (before + inc - n);
+      const int64_t i = item - (before + inc - n);
       if (i >= 0 && i < n) {
         found = Place{base + lane, (int)i / q.rt, (int)i % q.rt, 0};
         tiles = q.tiles;
@@ -214,8 +221,8 @@ __device__ __forceinline__ void find_item(const Kv4Params &p, Piece &pc) {
     }
   }
   __syncthreads();
-  const int n = tiles, each = (n + S::WARPS - 1) / S::WARPS;  // tiles of a warp
-  const int first = min(warp * each, n), last = min(first + each, n);
+  const int n = tiles, warps = S::WARPS * p.cluster, each = (n + warps - 1) / warps;  // tiles of a warp
+  const int first = min((warp * p.cluster + rank) * each, n), last = min(first + each, n);
   pc = Piece{};
   pc.at = found;
   pc.at.off = S::START + first;
@@ -474,6 +481,29 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ int4 as_int4(uint4 v) { return make_int4((int)v.x, (int)v.y, (int)v.z, (int)v.w); }
+__device__ __forceinline__ float4 as_float4(uint4 v) {
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t u;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(addr) : "memory");
@@ -547,8 +577,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t *ring = smem + warp * STAGES * S::STAGE;
-  __shared__ float2 warp_ml[WARPS][R];
-  __shared__ int4 warp_held[WARPS];
+  __shared__ float2 warp_ml[WARPS][R], cta_ml[R];
+  __shared__ int4 warp_held[WARPS], cta_held;
   // What the loop over the tiles does not need waits in shared memory, so that
   // the loop keeps its operands in registers.
   __shared__ Walk walks[WARPS];
@@ -985,8 +1015,11 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
 #pragma unroll
     for (int w = 1; w < WARPS; ++w)
       if (d.w == 0) d = warp_held[w];  // (a warp may have had none of its tiles)
-    const bool all = pc.complete(S::START);
+    const bool all = pc.complete(S::START), clustered = p.cluster > 1;
+    // the CTA's partial: its own shared memory (behind warp 0's part), or the workspace
     const int64_t part = (int64_t)blockIdx.x * WARPS * 2 * R;
+    float *const cta_o = clustered ? reinterpret_cast<float *>(smem) + R * D : p.ws_o + part * D;
+    float2 *const to_ml = clustered ? cta_ml : p.ws_ml + part;
     for (int i = tid; i < d.w * (D / 4); i += THREADS) {
       const int row = i / (D / 4), dim = (i % (D / 4)) * 4;
       float m = kNoRef, l = 0.f;
@@ -1008,7 +1041,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
         o.z = fmaf(f, v.z, o.z);
         o.w = fmaf(f, v.w, o.w);
       }
-      if (all) {
+      if (all && !clustered) {
         const bool none = saw_none(m, l);
         const float inv = none ? 0.f : 1.f / l;
         const int64_t at = out_row(p, d.x, d.y, d.z + row);
@@ -1016,9 +1049,53 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         if (dim == 0) p.lse[at] = none ? -INFINITY : (m + log2f(l)) * kLn2;
       } else {
-        *reinterpret_cast<float4 *>(p.ws_o + (part + row) * D + dim) = o;
-        if (dim == 0) p.ws_ml[part + row] = make_float2(m, l);
+        *reinterpret_cast<float4 *>(cta_o + row * D + dim) = o;
+        if (dim == 0) to_ml[row] = make_float2(m, l);
       }
+    }
+    if (clustered) {
+      // The CTAs' partials, merged by all of them.  Every CTA of the cluster is here: they share one item.  The first
+      // one's first warp has the item's first tile, so it knows the rows.
+      if (tid == 0) cta_held = d;
+      __syncwarp();
+      cluster_sync_all();
+      const uint32_t o_s = smem_u32(cta_o), ml_s = smem_u32(cta_ml), held_s = smem_u32(&cta_held);
+      d = as_int4(ld_cluster_v4(mapa_shared(held_s, 0)));
+      const int rank = (int)cluster_ctarank();
+      for (int i = rank * THREADS + tid; i < d.w * (D / 4); i += p.cluster * THREADS) {
+        const int row = i / (D / 4), dim = (i % (D / 4)) * 4;
+        float2 ml[kMostCluster];
+        float4 v[kMostCluster];
+        float m = kNoRef, l = 0.f;
+#pragma unroll
+        for (int c = 0; c < kMostCluster; ++c) {
+          ml[c] = make_float2(kNoRef, 0.f);
+          v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c >= p.cluster || ld_cluster_u32(mapa_shared(held_s + 12, c)) == 0) continue;  // (.w: a CTA without a tile)
+          ml[c] = ld_cluster_f2(mapa_shared(ml_s + row * 8, c));
+          v[c] = as_float4(ld_cluster_v4(mapa_shared(o_s + (row * D + dim) * 4, c)));
+          m = fmaxf(m, ml[c].x);
+        }
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kMostCluster; ++c) {
+          if (saw_none(ml[c].x, ml[c].y)) continue;
+          const float f = ex2_approx(ml[c].x - m);
+          l = fmaf(f, ml[c].y, l);
+          o.x = fmaf(f, v[c].x, o.x);
+          o.y = fmaf(f, v[c].y, o.y);
+          o.z = fmaf(f, v[c].z, o.z);
+          o.w = fmaf(f, v[c].w, o.w);
+        }
+        const bool none = saw_none(m, l);
+        const float inv = none ? 0.f : 1.f / l;
+        const int64_t at = out_row(p, d.x, d.y, d.z + row);
+        *reinterpret_cast<uint2 *>(p.o + at * D + dim) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (dim == 0) p.lse[at] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+      }
+      __syncwarp();
+      cluster_sync_all();  // no CTA leaves while another reads its shared memory
     }
   }
   if (lane == 0 && p.pieces > 0) {
@@ -1183,35 +1260,78 @@ __global__ void __launch_bounds__(kMergeThreads) attn_kv4_merge_kernel(const Kv4
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 
+// A launch of `ctas` CTAs in clusters of `cluster`.
 template <typename S>
-cudaError_t prepare(int device) {
+struct ClusterLaunch {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  ClusterLaunch(int64_t ctas, int cluster, cudaStream_t st) {
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(S::THREADS);
+    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.stream = st;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+  }
+};
+
+// Once a device: the kernel's shared memory, and how many clusters of 2, 4 and 8
+// CTAs the device holds at once (fewer than its SMs would give: a cluster does
+// not reach over the device's groups of SMs).
+template <typename S>
+cudaError_t prepare(int device, const int **held) {
   static bool done[kMaxDevices];
+  static int most[kMaxDevices][kClusterSizes];
   std::lock_guard<std::mutex> lock(g_mu);
   if (!done[device]) {
     const cudaError_t e =
         cudaFuncSetAttribute(attn_kv4_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
+    for (int i = 0; i < kClusterSizes; ++i) {
+      ClusterLaunch<S> launch(2 << i, 2 << i, nullptr);
+      if (cudaOccupancyMaxActiveClusters(&most[device][i], attn_kv4_kernel<S>, &launch.cfg) != cudaSuccess) {
+        cudaGetLastError();
+        most[device][i] = 0;
+      }
+    }
     done[device] = true;
   }
+  *held = most[device];
   return cudaSuccess;
 }
 
 template <typename S>
 int launch_kv4(Kv4Params &p, int device, int sms, cudaStream_t st) {
-  cudaError_t e = prepare<S>(device);
+  const int *held = nullptr;  // clusters of 2, 4, 8 that the device holds at once
+  cudaError_t e = prepare<S>(device, &held);
   if (e != cudaSuccess) return record_cuda_error(e);
-  // What the lengths can be at most: one CTA for each item where these are few
-  // and short, else one per SM, and no more pieces than there can be units.
-  const int64_t row_tiles = (int64_t)p.T * p.group / S::R + p.B;
+  // What the lengths can be at most.  A request's query tokens fill no more row
+  // tiles than each of them alone would, and one more than its rows / R.
+  const int64_t by_rows = (int64_t)p.T * p.group / S::R + p.B, by_token = (int64_t)p.T * ((p.group + S::R - 1) / S::R);
   const int64_t tiles = ((int64_t)p.max_pages * S::P + S::TK - 1) / S::TK + 1;
-  const int64_t items = row_tiles * p.H;
+  const int64_t items = (by_rows < by_token ? by_rows : by_token) * p.H;
   if (items > ((int64_t)1 << 40) / (tiles + S::START)) return ATTN_ERR_ARG;  // a piece's units are 32-bit
-  if (items <= sms && tiles <= 4 * S::WARPS) {
+  // Few and short items have a cluster of CTAs each: the most (a power of two up
+  // to 8) that leaves each warp a tile and all clusters resident at once (a second
+  // wave costs more than it gives: 32 items of 2000 tokens 10.3 us in clusters of
+  // 4, 28.1 of 8), and no second kernel while a warp has at most 8 tiles.  Against
+  // pieces (D 128, 8 kv heads): 1 request of 2000 tokens 9.8 us against 13.2, of
+  // 8000 13.1 against 13.9, 4 of 4000 12.8 against 16.4, 8 of 2000 12.4 against
+  // 16.5, 16 of 2000 15.7 against 19.8.  At up to 16 tiles a warp, requests of
+  // other lengths than the longest wait for it: 16 of 4000 and less 21.8 against
+  // 18.6.
+  p.cluster = 1;
+  for (int i = 0; i < kClusterSizes && tiles > S::WARPS * p.cluster && items <= held[i]; ++i) p.cluster *= 2;
+  if (items <= sms && tiles <= 8 * S::WARPS * p.cluster) {
     p.pieces = 0;
-    attn_kv4_kernel<S><<<(unsigned)items, S::THREADS, S::SMEM, st>>>(p);
-    e = cudaGetLastError();
+    const ClusterLaunch<S> launch(items * p.cluster, p.cluster, st);
+    e = cudaLaunchKernelEx(&launch.cfg, attn_kv4_kernel<S>, (const Kv4Params)p);
     return e == cudaSuccess ? ATTN_OK : record_cuda_error(e);
   }
+  p.cluster = 1;
   const int64_t most = (items * (tiles + S::START) + S::WARPS - 1) / S::WARPS;
   const int grid = (int)(most < sms ? most : sms);
   p.pieces = grid * S::WARPS;

@@ -284,6 +284,34 @@ def test_attention_matches_oracle(case, causal):
     _run(list(lens), list(nq), Hq, H, D, P, causal=causal, seed=sum(lens) + D)
 
 
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"{len(c[0])}x{max(c[0])}q{max(c[1])}h{c[2]}k{c[3]}d{c[4]}p{c[5]}")
+def test_attention_under_a_table_for_long_contexts(case):
+    # items cut into pieces and merged by the second kernel, whatever the lengths
+    _run(*map(list, case[:2]), *case[2:], width=80000 // case[5], pad=2)
+
+
+@pytest.mark.parametrize("lens,nq,Hq,H,D,P,width", [
+    ((2900,), (1,), 8, 1, 128, 16, None), ((2900,), (1,), 8, 1, 128, 16, 800), ((7000,), (2,), 3, 1, 64, 32, None),
+    ((33, 0, 5), (1, 1, 1), 8, 2, 128, 16, 150), ((1, 2000, 0, 700), (1, 1, 0, 2), 4, 2, 64, 16, None),
+    ((1800, 40), (1, 5), 4, 1, 192, 16, None), ((3500,), (1,), 4, 2, 256, 64, None), ((900, 1500), (5, 3), 8, 2, 256, 32, None),
+    ((1500, 900), (70, 66), 4, 1, 64, 16, None), ((1500, 900), (70, 20), 4, 1, 128, 64, None), ((9000,), (1,), 5, 1, 128, 64, None),
+    ((1200,) * 9, (1,) * 9, 16, 4, 128, 16, None)], ids=str)
+def test_items_spread_over_a_cluster(lens, nq, Hq, H, D, P, width):
+    _run(list(lens), list(nq), Hq, H, D, P, seed=len(lens) + D, width=width, pad=1)
+
+
+def test_a_cluster_gives_the_same_bits_every_time():
+    H, D, P = 2, 128, 16
+    cache = _random_cache(200, H, D, P, 7)
+    q = _randn((3, 8, D), 8)
+    dev = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    args = (q, dev([0, 1, 2, 3]), dev([3100, 900, 17]), dev([list(range(200))] * 3), cache, P)
+    o, lse = attn_fwd_kv4(*args)
+    for _ in range(20):
+        a, b = attn_fwd_kv4(*args)
+        assert torch.equal(a, o) and torch.equal(b, lse)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.07, 3.0])
 def test_attention_scales(scale):
     _run([150, 33], [1, 2], 8, 2, 128, 16, scale=scale, seed=3)
