@@ -44,8 +44,8 @@
 // workspace, which a second kernel -- launched early, its wait overlapping the
 // first's end -- merges in the order of the tokens.  Where one item covers all
 // the pieces of a CTA its warps' parts are merged in shared memory first.
-// Where the items are few and short by the sizes alone (no more than SMs, at
-// most 8 tiles a warp), each has a cluster of 1 to 8 CTAs, whose parts are merged
+// Where the items are few and short by the sizes alone (no more than SMs, a few
+// tiles a warp), each has a cluster of 1 to 8 CTAs, whose parts are merged
 // through distributed shared memory, and there is no workspace and no second
 // kernel: one request of 129 tokens 6.4 us against 9.8, 8 requests of 1000 9.9
 // against 14.2, 4 of 4000 12.8 against 16.4.
@@ -1317,17 +1317,19 @@ int launch_kv4(Kv4Params &p, int device, int sms, cudaStream_t st) {
   // Few and short items have a cluster of CTAs each: the most (a power of two up
   // to 8) that leaves each warp a tile and all clusters resident at once (a second
   // wave costs more than it gives: 32 items of 2000 tokens 10.3 us in clusters of
-  // 4, 28.1 of 8), and no second kernel while a warp has at most 8 tiles.  Against
-  // pieces (D 128, 8 kv heads): 1 request of 2000 tokens 9.8 us against 13.2, of
-  // 8000 13.1 against 13.9, 4 of 4000 12.8 against 16.4, 8 of 2000 12.4 against
-  // 16.5, 16 of 2000 15.7 against 19.8.  At up to 16 tiles a warp, requests of
-  // other lengths than the longest wait for it: 16 of 4000 and less 21.8 against
-  // 18.6.
+  // 4, 28.1 of 8), and no second kernel.  Pieces would have each warp's tiles done
+  // by all SMs, but cost about two tiles' time more.  Against pieces (D 128, 8 kv
+  // heads): 1 request of 2000 tokens 9.8 us against 13.2, of 8000 13.3 against
+  // 14.1, of 16000 (5 tiles a warp, 64 of 152 SMs) 17.2 against 16.5, 4 of 4000 12.8
+  // against 16.4, 8 of 2000 12.4 against 16.5, 16 of 2000 15.7 against 19.8.  Above 8
+  // tiles a warp, shorter requests' warps wait for the longest: 16 of 4000 and
+  // less 21.8 against 18.6.
   p.cluster = 1;
   for (int i = 0; i < kClusterSizes && tiles > S::WARPS * p.cluster && items <= held[i]; ++i) p.cluster *= 2;
-  if (items <= sms && tiles <= 8 * S::WARPS * p.cluster) {
+  const int64_t ctas = items * p.cluster, warps = S::WARPS * p.cluster;  // of all items, of one item
+  if (items <= sms && tiles <= 8 * warps && tiles * (sms - ctas) <= 2 * sms * warps) {
     p.pieces = 0;
-    const ClusterLaunch<S> launch(items * p.cluster, p.cluster, st);
+    const ClusterLaunch<S> launch(ctas, p.cluster, st);
     e = cudaLaunchKernelEx(&launch.cfg, attn_kv4_kernel<S>, (const Kv4Params)p);
     return e == cudaSuccess ? ATTN_OK : record_cuda_error(e);
   }

@@ -484,10 +484,10 @@ ATTN_API int attn_kv4_read(const void *cache, int num_pages, const int *slots, v
  *
  * Asynchronous on `stream`: one launch where the items ((T * Hq / Hkv / 8 + B) *
  * Hkv by the sizes, or T * Hkv where Hq / Hkv <= 8, if that is less) are no more
- * than the SMs and max_pages * page_size is at most some 2000 to 4000 tokens, by
- * head dim, and up to 8 times that for fewer items (thread-block clusters); else
- * two launches and a stream-ordered workspace of at most 21 MB (152 SMs) from the
- * library's pool (ATTN_ERR_NOMEM if it cannot be had).  CUDA graphs: as attn_fwd; the grid depends on the sizes
+ * than the SMs and max_pages * page_size is at most a few thousand tokens, by head
+ * dim and the number of items (each is a thread-block cluster); else two launches
+ * and a stream-ordered workspace of at most 21 MB (152 SMs) from the library's
+ * pool (ATTN_ERR_NOMEM if it cannot be had).  CUDA graphs: as attn_fwd; the grid depends on the sizes
  * alone, so a replay may have other lengths, tables and query counts.
  * Deterministic for given lengths on a given device.
  */
