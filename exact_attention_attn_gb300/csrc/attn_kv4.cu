@@ -955,8 +955,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
       cut_last = (int)((done.end - 1) / pc.chunk);
       const int64_t last_begin = (int64_t)(cut_last / pc.warps) * pc.warps * pc.chunk;
       const int64_t last_end = min(last_begin + pc.warps * pc.chunk, pc.total);
-      cut_flags = (part_s ? 1 : 0) |
-                  (cut_last / pc.warps != (int)blockIdx.x && done.end >= last_end && last_begin + pc.chunk < last_end ? 2 : 0);
+      const bool last_s =
+          cut_last / pc.warps != (int)blockIdx.x && done.end >= last_end && last_begin + pc.chunk < last_end;
+      cut_flags = (part_s ? 1 : 0) | (last_s ? 2 : 0);
     }
     // a shared item's part goes to shared memory (this warp's ring, empty by now)
     const int64_t part = ((int64_t)piece * 2 + (done.tile0 > 0 ? 0 : 1)) * R;
@@ -1071,7 +1072,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
         for (int c = 0; c < kMostCluster; ++c) {
           ml[c] = make_float2(kNoRef, 0.f);
           v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (c >= p.cluster || ld_cluster_u32(mapa_shared(held_s + 12, c)) == 0) continue;  // (.w: a CTA without a tile)
+          // (.w: a CTA without a tile)
+          if (c >= p.cluster || ld_cluster_u32(mapa_shared(held_s + 12, c)) == 0) continue;
           ml[c] = ld_cluster_f2(mapa_shared(ml_s + row * 8, c));
           v[c] = as_float4(ld_cluster_v4(mapa_shared(o_s + (row * D + dim) * 4, c)));
           m = fmaxf(m, ml[c].x);
@@ -1404,8 +1406,8 @@ int attn_fwd_kv4(const void *q, long long q_stride_t, long long q_stride_h, cons
   if ((max_pages > 0 && !block_table) || (num_pages > 0 && !cache)) return ATTN_ERR_ARG;
   if (q_stride_t < 0 || q_stride_h < 0) return ATTN_ERR_ARG;
   if (off16(q) || off16(o) || off16(lse) || off16(cache) || q_stride_t % 8 || q_stride_h % 8) return ATTN_ERR_ALIGN;
-  if ((reinterpret_cast<uintptr_t>(cu) | reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(block_table)) & 3u)
-    return ATTN_ERR_ALIGN;
+  for (const int *a : {cu, lens, block_table})
+    if (reinterpret_cast<uintptr_t>(a) & 3u) return ATTN_ERR_ALIGN;
   int device = 0, sms = 0;
   Kv4Params p{};
   const int rc = current_device(&device, &sms, &p.status);
