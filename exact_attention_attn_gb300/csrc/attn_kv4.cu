@@ -28,9 +28,11 @@
 // Softmax.  p = 2^(y - ref), ref a per-row reference 10 above which the warp
 // rescales only when some y exceeds ref + 15; P s' is rounded to half
 // precision (2^-11 relative; bfloat16's 2^-8 would be as large as the output's own
-// rounding) after dividing by a power of two that tracks the group's
-// largest scale, so that its products keep 11 bits down to 2^-24 of the
-// largest.  l and the sums of p m' are in float32.
+// rounding) times a power of two of the row's and group's own.  That follows the
+// largest scale s' which the row has seen, but never takes the row's products so
+// low that a rounding passes 2^-28 of their sum: a token that is hidden from the
+// row, or that it gives no weight, cannot take the others' bits, however large its
+// V is.  l and the sums of p m' are in float32.
 //
 // Work split.  The tiles of all (request, kv head, row tile) items form one
 // line, cut into equal pieces, one per resident warp: lengths are read on the
@@ -83,6 +85,9 @@ constexpr int kMostCluster = 1 << kClusterSizes;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoRef = -1e37f;  // reference of a row that has seen no key
+constexpr int kMostSig = 100;     // exponent of a row's power of two before its first product
+constexpr int kLeastTop = 4;      // a row's products reach 2^(kLeastTop - 1) before their rounding, at least
+constexpr uint32_t kBias = 4000;  // added to exponents, so that they are not negative
 constexpr int kMaxRequests = ATTN_KV4_MAX_REQUESTS;
 
 struct Kv4Params {
@@ -707,7 +712,10 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
     }
 
     float acc[NT][G][4][4];  // O^T: [row tile][group][dim tile][c]
-    float ref[NT][2], l[NT][2], vm[NT][G][2], isig[G];
+    float ref[NT][2], l[NT][2], vm[NT][G][2];
+    // the power of two that a row's weighted scales of V are brought to half precision by (0: a row that sees nothing
+    // here), and the rows' largest
+    float isig[NT][G][2], top_sig[G];
     int lim[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -717,6 +725,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
         l[nt][c] = 0.f;
         const int row = row0 + nt * 8 + 2 * t + c;
         lim[nt][c] = row < rows ? it.limit(row, p) : 0;
+#pragma unroll
+        for (int j = 0; j < G; ++j) isig[nt][j][c] = lim[nt][c] > it.tile0 * TK ? pow2(kMostSig) : 0.f;
       }
 #pragma unroll
       for (int j = 0; j < G; ++j) {
@@ -726,7 +736,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
       }
     }
 #pragma unroll
-    for (int j = 0; j < G; ++j) isig[j] = 0x1p100f;
+    for (int j = 0; j < G; ++j) top_sig[j] = pow2(kMostSig);
 
     for (int tile = it.tile0; tile < stop; ++tile) {
       cp_async_wait<STAGES - 1>();
@@ -795,8 +805,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
               if (ta + hf * 16 >= it.q.len) pv[hf][j][0] = 0u;
               if (ta + hf * 16 + 8 >= it.q.len) pv[hf][j][1] = 0u;
             }
-            big_v = max3f(big_v, __uint_as_float(pv[hf][j][0] << 16) * isig[j],
-                          __uint_as_float(pv[hf][j][1] << 16) * isig[j]);
+            big_v = max3f(big_v, __uint_as_float(pv[hf][j][0] << 16) * top_sig[j],
+                          __uint_as_float(pv[hf][j][1] << 16) * top_sig[j]);
           }
         // e = y - ref in log2 units; hidden tokens -inf (selected, so that nothing they hold is used)
         float e[2][NT][4];
@@ -817,28 +827,30 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
               top = max3f(top, ea, eb);
             }
         if (__any_sync(0xffffffffu, top > 15.f || big_v > 1.9f)) {  // move the references up
-          float fs[G];
+          // Exponents (biased by 127) of the scales that are numbers, in both halves of a word, and of the largest of a
+          // group; those of the rows' new powers of two
+          uint32_t es[G][2][2];
+          int big[G], most[G];
 #pragma unroll
           for (int j = 0; j < G; ++j) {
-            float big = 0.f;  // from the scales themselves: over the old power of two they may have overflowed
+            big[j] = 0;
+            most[j] = -127;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const float s = __uint_as_float(pv[hf][j][c] << 16);
-                big = fmaxf(big, s < INFINITY ? s : 0.f);
+              for (int u = 0; u < 2; ++u) {
+                const uint32_t s = pv[hf][j][u] << 16;
+                const int ex = s < 0x7f800000u ? s >> 23 : 0;
+                es[j][hf][u] = ex * 0x10001u;
+                big[j] = max(big[j], ex);
               }
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-            fs[j] = 1.f;
-            if (big * isig[j] > 1.f) {  // the largest scale becomes [0.5, 1)
-              const float now = pow2(max(-126, -1 - exp_of(big)));
-              fs[j] = now / isig[j];
-              isig[j] = now;
-            }
+            big[j] = __reduce_max_sync(0xffffffffu, big[j]);
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt) {
+            float down[2], f[2];
+            uint32_t ey[2][2][2];  // [half][token][row]: exponent of the token's weight, far down where it is hidden
+            int up[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               float m = -INFINITY;
@@ -850,24 +862,64 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
               const float now = fmaxf(ref[nt][c], m - 10.f);
-              const float f = ex2_approx(ref[nt][c] - now);
+              down[c] = ref[nt][c] - now;
+              f[c] = ex2_approx(down[c]);
+              up[c] = (int)ceilf(fminf(-down[c], 300.f));  // whole powers of two that the weights have shrunk by
               ref[nt][c] = now;
+              l[nt][c] *= f[c];
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-                for (int u = c; u < 4; u += 2)
-                  if (e[hf][nt][u] != -INFINITY) e[hf][nt][u] = fmaf(x[hf][nt][u], fac[nt][c], -now);
-              l[nt][c] *= f;
+                for (int u = 0; u < 2; ++u) {
+                  float &y = e[hf][nt][2 * u + c];
+                  const bool seen = y != -INFINITY;
+                  if (seen) y = fmaf(x[hf][nt][2 * u + c], fac[nt][c], -now);
+                  // (the bits of 1.5 * 2^23 + y are those of 1.5 * 2^23, plus y's nearest whole number)
+                  const uint32_t whole = __float_as_uint(fminf(fmaxf(y, -1000.f), 100.f) + 12582912.f) - 0x4b400000u;
+                  ey[hf][u][c] = seen ? whole + kBias : kBias - 2000u;
+                }
+            }
 #pragma unroll
-              for (int j = 0; j < G; ++j) {
-                vm[nt][j][c] *= f;
+            for (int j = 0; j < G; ++j) {
+              // The exponent of the largest weighted scale that each row sees here (row c in half c), or of what it has
+              // summed so far over the largest code.
+              uint32_t key = 0;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float held = 0.f;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) held = max3f(held, acc[nt][j][d][c], acc[nt][j][d][2 + c]);
+                key |= (uint32_t)(exp_of(held) + 127 + 20 - exp_of(isig[nt][j][c]) - up[c] + (int)kBias) << (16 * c);
+              }
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) key = __vmaxu2(key, es[j][hf][u] + ey[hf][u][0] + (ey[hf][u][1] << 16));
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) key = __vmaxu2(key, __shfl_xor_sync(0xffffffffu, key, o));
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                vm[nt][j][c] *= f[c];
+                // The largest scale becomes [0.5, 1), so that no weight up to 2^15 overflows, unless that took the
+                // row's largest product too low; what the row has summed keeps its place where that falls.
+                const int old = exp_of(isig[nt][j][c]);
+                const int low = min(old, 126 - big[j]);
+                const int need = kLeastTop + 127 + (int)kBias - (int)(c ? key >> 16 : key & 0xffffu);
+                const int next = old == -127 ? old : max(-126, min(min(old + up[c], kMostSig), max(low, need)));
+                const float by =
+                    next <= old ? f[c] * pow2(max(next - old, -126)) : ex2_approx(down[c] + (float)(next - old));
+                isig[nt][j][c] = pow2(next);
+                most[j] = max(most[j], next);
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
-                  acc[nt][j][d][c] *= f * fs[j];
-                  acc[nt][j][d][2 + c] *= f * fs[j];
+                  acc[nt][j][d][c] *= by;
+                  acc[nt][j][d][2 + c] *= by;
                 }
               }
             }
+          }
+#pragma unroll
+          for (int j = 0; j < G; ++j) top_sig[j] = pow2(__reduce_max_sync(0xffffffffu, most[j]));
         }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -884,12 +936,15 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
 #pragma unroll
           for (int j = 0; j < G; ++j) {
             const uint32_t pa = pv[hf][j][0], pb = pv[hf][j][1];
-            const float ua = __uint_as_float(pa << 16) * isig[j], ub = __uint_as_float(pb << 16) * isig[j];
+            const float sa = __uint_as_float(pa << 16), sb = __uint_as_float(pb << 16);
             const float ma = __uint_as_float(pa & 0xffff0000u), mb = __uint_as_float(pb & 0xffff0000u);
             uint32_t b0[NT], b1[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float w[4] = {pr[nt][0] * ua, pr[nt][1] * ua, pr[nt][2] * ub, pr[nt][3] * ub};
+              float w[4];
+              const uint64_t up = f2_pack(isig[nt][j][0], isig[nt][j][1]);
+              f2_unpack(f2_mul(f2_pack(pr[nt][0], pr[nt][1]), f2_mul(f2_pack(sa, sa), up)), w[0], w[1]);
+              f2_unpack(f2_mul(f2_pack(pr[nt][2], pr[nt][3]), f2_mul(f2_pack(sb, sb), up)), w[2], w[3]);
               if (!edge) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) vm[nt][j][c] = fmaf(pr[nt][2 + c], mb, fmaf(pr[nt][c], ma, vm[nt][j][c]));
@@ -981,7 +1036,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
 #pragma unroll
         for (int j = 0; j < G; ++j) {
           // 1 / isig, a power of two as isig is
-          const float sig = __uint_as_float((254u << 23) - __float_as_uint(isig[j])), m = vm[nt][j][c];
+          const float sig = __uint_as_float((254u << 23) - __float_as_uint(isig[nt][j][c])), m = vm[nt][j][c];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float o[4];

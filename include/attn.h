@@ -464,9 +464,10 @@ ATTN_API int attn_kv4_read(const void *cache, int num_pages, const int *slots, v
  * cu, lens, block_table  device, int32, as attn_pages_assign makes them.
  * D      64, 128, 192 or 256.  page_size, num_pages, max_pages, table_stride as
  *        above.  B is 0 .. ATTN_KV4_MAX_REQUESTS.
- * scale  finite.  Products are exact on the codes (fp32 accumulation); the
- *        probabilities are rounded to 11 bits before the second product, O
- *        once to bf16.
+ * scale  finite.  Products are exact on the codes (fp32 accumulation); a
+ *        probability times V's scale is rounded to 11 bits before the second
+ *        product (to 2^-28 of the row's sum of these over its keys, where that
+ *        is coarser), O once to bf16.
  * Made for few query rows (query tokens x Hq / Hkv up to about 64 a request).
  * More work as well, at about 200 TFLOP/s; a long prompt chunk over a cached
  * prefix is better served by attn_kv4_read and attn_fwd.
