@@ -85,8 +85,13 @@ constexpr int kMostCluster = 1 << kClusterSizes;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoRef = -1e37f;  // reference of a row that has seen no key
-constexpr int kMostSig = 100;     // exponent of a row's power of two before its first product
+constexpr int kMostSig = 126;     // exponent of a row's power of two before its first product
 constexpr int kLeastTop = 4;      // a row's products reach 2^(kLeastTop - 1) before their rounding, at least
+// What multiplies the weights (up to 2^15) in O's sums, so that these do not
+// overflow before they are divided by l.  A smaller one would cost values near
+// 2^-126 their bits: a term's rounding of 2^-150 over a largest weight of 2^-15
+// is 2^-135, less than half of bfloat16's last place.
+constexpr float kDown = 0x1p-25f;
 constexpr uint32_t kBias = 4000;  // added to exponents, so that they are not negative
 constexpr int kMaxRequests = ATTN_KV4_MAX_REQUESTS;
 
@@ -923,7 +928,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
         }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          float pr[NT][4];
+          float pr[NT][4], pm[NT][4];  // weights, and what multiplies the minima
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -931,6 +936,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
               pr[nt][c] = ex2_approx(e[hf][nt][c]);
               pr[nt][2 + c] = ex2_approx(e[hf][nt][2 + c]);
               l[nt][c] += pr[nt][c] + pr[nt][2 + c];
+              pm[nt][c] = pr[nt][c] * kDown;
+              pm[nt][2 + c] = pr[nt][2 + c] * kDown;
             }
           // O^T += V^T P^T
 #pragma unroll
@@ -947,14 +954,14 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
               f2_unpack(f2_mul(f2_pack(pr[nt][2], pr[nt][3]), f2_mul(f2_pack(sb, sb), up)), w[2], w[3]);
               if (!edge) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) vm[nt][j][c] = fmaf(pr[nt][2 + c], mb, fmaf(pr[nt][c], ma, vm[nt][j][c]));
+                for (int c = 0; c < 2; ++c) vm[nt][j][c] = fmaf(pm[nt][2 + c], mb, fmaf(pm[nt][c], ma, vm[nt][j][c]));
               } else {  // a hidden token's scale and minimum may be anything
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                   const bool no_a = e[hf][nt][c] == -INFINITY, no_b = e[hf][nt][2 + c] == -INFINITY;
                   if (no_a) w[c] = 0.f;
                   if (no_b) w[2 + c] = 0.f;
-                  vm[nt][j][c] = fmaf(pr[nt][2 + c], no_b ? 0.f : mb, fmaf(pr[nt][c], no_a ? 0.f : ma, vm[nt][j][c]));
+                  vm[nt][j][c] = fmaf(pm[nt][2 + c], no_b ? 0.f : mb, fmaf(pm[nt][c], no_a ? 0.f : ma, vm[nt][j][c]));
                 }
               }
               b0[nt] = transpose8x8(half2_bits(w[0], w[1]));
@@ -1031,7 +1038,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
         const int row = nt * 8 + 2 * t + c, q = row0 + row;
         if (q >= rows) continue;
         const bool none = saw_none(ref[nt][c], l[nt][c]);
-        const float inv = whole ? (none ? 0.f : __frcp_rn(l[nt][c])) : 1.f;
+        const float inv = whole ? (none ? 0.f : __frcp_rn(l[nt][c]) / kDown) : 1.f;
         const int64_t at = out_row(p, done.q.t0, done.h, q);
 #pragma unroll
         for (int j = 0; j < G; ++j) {
@@ -1042,8 +1049,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
             float o[4];
 #pragma unroll
             for (int d = 0; d < 2; ++d) {
-              o[2 * d] = fmaf(acc[nt][j][2 * k + d][c] * 0x1p24f, sig, m) * inv;
-              o[2 * d + 1] = fmaf(acc[nt][j][2 * k + d][2 + c] * 0x1p20f, sig, m) * inv;
+              o[2 * d] = fmaf(acc[nt][j][2 * k + d][c] * (0x1p24f * kDown), sig, m) * inv;
+              o[2 * d + 1] = fmaf(acc[nt][j][2 * k + d][2 + c] * (0x1p20f * kDown), sig, m) * inv;
             }
             const int dim = j * kKv4Group + k * 32 + g * 4;
             if (whole)
@@ -1099,7 +1106,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
       }
       if (all && !clustered) {
         const bool none = saw_none(m, l);
-        const float inv = none ? 0.f : 1.f / l;
+        const float inv = none ? 0.f : 1.f / kDown / l;
         const int64_t at = out_row(p, d.x, d.y, d.z + row);
         *reinterpret_cast<uint2 *>(p.o + at * D + dim) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -1145,7 +1152,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
           o.w = fmaf(f, v[c].w, o.w);
         }
         const bool none = saw_none(m, l);
-        const float inv = none ? 0.f : 1.f / l;
+        const float inv = none ? 0.f : 1.f / kDown / l;
         const int64_t at = out_row(p, d.x, d.y, d.z + row);
         *reinterpret_cast<uint2 *>(p.o + at * D + dim) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -1300,7 +1307,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_kv4_merge_kernel(const Kv4
     }
     if (mine && sub == 0) {
       const bool none = saw_none(m, l);
-      const float inv = none ? 0.f : 1.f / l;
+      const float inv = none ? 0.f : 1.f / kDown / l;
       const int64_t at = out_row(p, d.x, d.y, d.z + row);
 #pragma unroll
       for (int v = 0; v < V; ++v)

@@ -172,3 +172,34 @@ def test_groups_without_a_scale_beside_large_ones(wide):
     v[:150, 0] = -0.75
     v[60, 1, :64] *= 2.0 ** 70
     _run(k, v, _randn((4, 8, D), 19), P, wide)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_values_near_the_largest_number(shape, wide):
+    # |V| up to 2^126: sums of weighted values must not pass float32 before they are divided by the weights' sum
+    D, P, Hq, H = shape
+    n, nq = 700, 3
+    v = (_randn((n, H, D), 21) / 5).clamp(-1, 1) * 2.0 ** 126
+    out = _run(_randn((n, H, D), 20), v, _randn((nq, Hq, D), 22), P, wide)
+    assert torch.isfinite(out).all()
+    # one token alone has all the weight of a row
+    out = _run(_scored([0.0] * 40 + [90.0], H, D, 23), v[:41], torch.ones((1, Hq, D)), P, wide)
+    assert torch.isfinite(out).all()
+    # values in bfloat16's subnormals: the tolerance of their own last place
+    tiny = (_randn((200, H, D), 24) * 2.0 ** -125).to(torch.bfloat16)
+    k, q = _randn((200, H, D), 25).to(torch.bfloat16), _randn((1, Hq, D), 26).to(torch.bfloat16)
+    cache = attn_kv4_cache(-(-200 // P), H, D, P)
+    attn_kv4_append(k.cuda(), tiny.cuda(), _dev(range(200)), cache, P)
+    table = _dev([list(range(cache.shape[0])) + [-1] * (80000 // P if wide else 0)])
+    out, _ = attn_fwd_kv4(q.cuda(), _dev([0, 1]), _dev([200]), table, cache, P)
+    (kc, ks, km), (vc, vs, vm) = ([x.transpose(1, 0, 2, 3).reshape(H, -1, x.shape[3])[:, :200] for x in side]
+                                  for side in S.kv4_unpack(cache.cpu().numpy(), D, P))
+    kv, vv = S.kv4_values(kc, ks, km), S.kv4_values(vc, vs, vm)
+    for hq in range(Hq):
+        h = hq // (Hq // H)
+        x = D ** -0.5 * (kv[h] @ to_f64(q)[0, hq])
+        p = np.exp(x - x.max())
+        want = (p / p.sum()) @ vv[h]
+        # one step of bfloat16 (its own half, and the sums' below that)
+        assert (np.abs(to_f64(out)[0, hq] - want) <= 2.0 ** -133 + 2.0 ** -7 * np.abs(want)).all()
