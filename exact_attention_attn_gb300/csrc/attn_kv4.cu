@@ -863,7 +863,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
               for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
                 for (int u = c; u < 4; u += 2)
-                  if (e[hf][nt][u] != -INFINITY) m = fmaxf(m, x[hf][nt][u] * fac[nt][c]);
+                  if (e[hf][nt][u] != -INFINITY) m = fmaxf(m, __fmul_rn(x[hf][nt][u], fac[nt][c]));
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
               const float now = fmaxf(ref[nt][c], m - 10.f);
@@ -875,10 +875,25 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
+                for (int u = c; u < 4; u += 2)
+                  if (e[hf][nt][u] != -INFINITY) e[hf][nt][u] = fmaf(x[hf][nt][u], fac[nt][c], -now);
+              if (__any_sync(0xffffffffu, now > kNoRef && fabsf(now) >= 0x1p20f)) {
+                // The rounding of the product that gave the reference counts here: without it the largest score's y may
+                // be anything instead of 10, and its weight none or infinite.
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                  for (int u = c; u < 4; u += 2) {
+                    const float y = __fsub_rn(__fmul_rn(x[hf][nt][u], fac[nt][c]), now);
+                    if (e[hf][nt][u] != -INFINITY) e[hf][nt][u] = y > 15.f ? 15.f : y;
+                  }
+              }
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                  float &y = e[hf][nt][2 * u + c];
+                  const float y = e[hf][nt][2 * u + c];
                   const bool seen = y != -INFINITY;
-                  if (seen) y = fmaf(x[hf][nt][2 * u + c], fac[nt][c], -now);
                   // (the bits of 1.5 * 2^23 + y are those of 1.5 * 2^23, plus y's nearest whole number)
                   const uint32_t whole = __float_as_uint(fminf(fmaxf(y, -1000.f), 100.f) + 12582912.f) - 0x4b400000u;
                   ey[hf][u][c] = seen ? whole + kBias : kBias - 2000u;

@@ -203,3 +203,21 @@ def test_values_near_the_largest_number(shape, wide):
         want = (p / p.sum()) @ vv[h]
         # one step of bfloat16 (its own half, and the sums' below that)
         assert (np.abs(to_f64(out)[0, hq] - want) <= 2.0 ** -133 + 2.0 ** -7 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("power", [21, 27, 29, 36, 60])
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 32), (256, 64)])
+def test_scores_past_float32s_whole_numbers(D, P, power, wide):
+    # scores of about 2^power: one token has all the weight; float32 cannot hold a difference of ten beside them
+    n = 90
+    for at in (0, 50, 89):
+        size = torch.linspace(0.5, 0.75, n)
+        size[at] = 0.97
+        k = (size * 2.0 ** (power - 10))[:, None, None] / math.sqrt(D) * torch.ones((n, 1, D))
+        q = 2.0 ** 10 * torch.tensor([1.0, 0.9, -1.0])[None, :, None].expand(1, 3, D)
+        v = _randn((n, 1, D), 27)
+        out = _run(k, v, q, P, wide)
+        # V's own codes: within half a scale, and bfloat16's half step
+        near = (out[0, :2].float().cpu() - v[at].to(torch.bfloat16).float()).abs()
+        assert (near <= 0.55 * (v[at].max() - v[at].min()) / 15 + 0.02).all()
