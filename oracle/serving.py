@@ -102,17 +102,28 @@ def pages_release(table, lens, keep, free, count, P):
 
 # ---------------------------------------------------------------- the 4-bit cache
 
+def kv4_scale(m, hi):
+    """The scale of groups with minima m and maxima hi: the bfloat16 number nearest
+    to (hi - m) / 15, from float64.  Where that lies so close to the middle of two
+    numbers that float32 cannot tell (2^-22 relative), the format's own rule
+    decides: the float32 product of (hi - m) / 16, each step rounded, with the
+    float32 number nearest to 16 / 15, then rounded with ties to even."""
+    m, hi = np.asarray(m, dtype=np.float64), np.asarray(hi, dtype=np.float64)
+    f = np.float32
+    with np.errstate(over="ignore", invalid="ignore"):
+        exact = (hi - m) / 15
+        low, high = to_bf16(exact * (1 - 2.0 ** -22)), to_bf16(exact * (1 + 2.0 ** -22))
+        rule = ((hi / 16).astype(f) - (m / 16).astype(f)) * f(1 / 0.9375)
+        return np.where(low == high, to_bf16(exact), np.clip(to_bf16(rule.astype(np.float64)), low, high))
+
+
 def kv4_quantise(x):
     """x [..., D]: codes [..., D], scale and minimum [..., D / 64], and the exact
     quotients (x - m) / s that the codes round (0 where s = 0)."""
     x = np.asarray(x, dtype=np.float64)
     y = x.reshape(x.shape[:-1] + (x.shape[-1] // GROUP, GROUP))
     m, hi = y.min(-1), y.max(-1)
-    # in float32, by the reciprocal: where (max - m) / 15 lies halfway between two
-    # bfloat16 numbers, the product's rounding decides
-    f = np.float32
-    with np.errstate(over="ignore", invalid="ignore"):
-        s = to_bf16(((hi.astype(f) * f(0.0625) - m.astype(f) * f(0.0625)) * (f(1) / f(0.9375))).astype(np.float64))
+    s = kv4_scale(m, hi)
     q = np.where(s[..., None] > 0, (y - m[..., None]) / np.where(s > 0, s, 1.0)[..., None], 0.0)
     codes = np.clip(np.round(q), 0, 15).astype(np.int64)
     return codes.reshape(x.shape), s, m, q.reshape(x.shape)

@@ -1,10 +1,11 @@
 """The 4-bit cache and attention over it, against the float64 oracle.
 
-Codes, scales and minima are compared exactly: the scale is a quotient by 15
-whose float32 value cannot fall on a bfloat16 tie unless the exact one does, and
-a code may differ only where the exact quotient is within 2^-19 of a tie (the
-float32 difference x - m and the quotient are each off by at most 2^-24 of a
-value up to 15, twice).
+Codes, scales and minima are compared exactly: the oracle's scale is the bfloat16
+number nearest to the float64 quotient by 15, and where that is within float32's
+reach of a tie the one that the format's float32 product goes to; a code may
+differ only where the exact quotient is within 2^-19 of a tie (the float32
+difference x - m and the quotient are each off by at most 2^-24 of a value up to
+15, twice).
 
 Attention tolerance, per element, from the arithmetic:
   scores  float32 accumulation of exact products: at most 16 roundings (a tensor
@@ -14,9 +15,11 @@ Attention tolerance, per element, from the arithmetic:
   weights exp2 2^-22 relative, the weight rounded to half precision 2^-11
   output  float32 sums (2^-20 of the absolute sum), one rounding to bfloat16 2^-8
 so |dO| <= (2^-11 + 2 dS + 2^-19) A + 2^-8 |O|, A = softmax-weighted sum of s c + |m|,
-and |dLSE| <= dS + 2^-20 (1 + |LSE|).  (A weight below 2^-24 of the largest is in
-half precision's subnormals: 2^-35 of the largest weight times scale each, for
-n <= 2^14 tokens 2^-21 of it, inside the margin of the 2^-19.)"""
+and |dLSE| <= dS + 2^-20 (1 + |LSE|).  (A weight times scale in
+half precision's subnormals is off by 2^-25 at most, where the largest scale is in
+[1/2, 1) and the largest weight at least 2^10: with scales that differ by a factor
+of 2 at the heavy tokens, as here, 2^-33 of the products' sum each, for n <= 2^14
+tokens 2^-19 of it.  Caches whose scales differ by more are test_gpu_kv4_ranges'.)"""
 import math
 
 import numpy as np

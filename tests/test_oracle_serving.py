@@ -141,3 +141,34 @@ def test_kv4_unpack_and_attention():
     assert not np.allclose(S.attention_requests(q, cu, lens, table[:, ::-1], k, v, P, 0.1, True)[0][2:5], O[2:5])
     assert math.isclose(L[0, 0], float(torch.logsumexp(torch.from_numpy(
         np.concatenate([k[4, 0], k[1, 0]])[:20] @ q[0, 0] * 0.1), 0)))
+
+
+def test_kv4_scale_is_the_quotient_by_fifteen():
+    # against exact fractions: the nearest bfloat16 number, and at a tie (or within float32's reach of one) a neighbour
+    from fractions import Fraction
+    r = np.random.default_rng(21)
+    lo = S.to_bf16(-np.exp2(r.uniform(-130, 120, 4000)))
+    hi = S.to_bf16(-lo * np.exp2(r.uniform(-9, 9, 4000)))
+    for hi_, lo_ in ((1.8359375, -32.5), (34.25, -1.9609375), (34.0, -0.3359375), (2.28125 * 15 - 1, -1.0)):
+        hi, lo = np.append(hi, hi_), np.append(lo, lo_)
+    s, ties = S.kv4_scale(lo, hi), 0
+    for m, h, got in zip(lo, hi, s):
+        exact = (Fraction(float(h)) - Fraction(float(m))) / 15
+        step = Fraction(2) ** max(math.frexp(float(exact))[1] - 8, -133)
+        off = abs(Fraction(float(got)) - exact) / step
+        ties += off == Fraction(1, 2)
+        assert off <= Fraction(1, 2) + Fraction(1, 2 ** 13), (m, h, got)
+    assert ties >= 3
+
+
+def test_planted_mistakes_in_the_scale_are_seen():
+    # another factor, or a quotient that is cut instead of rounded, does not agree with the quotient by 15 (a factor
+    # nearer than some 2^-13 would: spans of 9 bits over 15 lie no closer to a tie)
+    r = np.random.default_rng(22)
+    x = S.to_bf16(r.standard_normal((200, 64)))
+    m, hi = x.min(-1), x.max(-1)
+    good = S.kv4_scale(m, hi)
+    for wrong in (np.float32(1.06), np.float32(17 / 16), np.float32(1.0)):
+        assert (S.to_bf16((hi - m) / 16 * float(wrong)) != good).any()
+    bits = ((hi - m) / 15).astype(np.float32).view(np.uint32) & np.uint32(0xffff0000)
+    assert (bits.view(np.float32) != good).any()
