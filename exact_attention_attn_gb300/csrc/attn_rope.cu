@@ -10,11 +10,12 @@
 //
 // The angle.  A float32 angle of position 10^6 is off by 0.03 rad, and float64
 // arithmetic is scarce on this chip.  The table holds theta_i / (2 pi) modulo
-// one turn as a 64-bit binary fraction f, so pos * f modulo 2^64 (one integer
-// multiply, wrapping) is the angle in turns without any rounding but the
-// table's: |pos| * 2^-53 relative to the fraction, below 2^-22 turns for every
-// int32 position.  Its upper 32 bits, read as a signed number, are the angle
-// in [-1/2, 1/2) turns; sincospif takes it as x = 2 * turns.
+// one turn as a 64-bit binary fraction f, rounded to nearest from the exact
+// value (whole turns of a large theta take no bits of it), so pos * f modulo
+// 2^64 (one integer multiply, wrapping) is the angle in turns without any
+// rounding but the table's: |pos| * 2^-65, at most 2^-34 turns for an int32
+// position.  Its upper 32 bits, read as a signed number, are the angle in
+// [-1/2, 1/2) turns; sincospif takes it as x = 2 * turns, a float32: 2^-26 turns.
 //
 // Work split.  A CTA takes NT tokens of one batch row, forms their rot/2 cos
 // and sin once in shared memory, and each thread then holds the 8 pairs of one
@@ -146,6 +147,91 @@ __global__ void __launch_bounds__(kThreads) attn_rope_kernel(const RopeParams p)
   }
 }
 
+// 1 / (2 pi) to kTurnWords * 32 binary places, most significant word last; a
+// double's whole turns (up to 2^971 of its last bits) are taken off by it.
+constexpr int kTurnWords = 40;
+
+// A number below 2^32 in fixed point: word kFixed - 1 is its whole part.
+constexpr int kFixed = 45;
+struct Fixed {
+  uint32_t w[kFixed];
+};
+
+void divide(Fixed &a, uint32_t by) {
+  uint64_t rest = 0;
+  for (int i = kFixed - 1; i >= 0; --i) {
+    rest = rest << 32 | a.w[i];
+    a.w[i] = (uint32_t)(rest / by);
+    rest %= by;
+  }
+}
+
+// a += sign * times * b
+void add(Fixed &a, const Fixed &b, int sign, uint32_t times) {
+  int64_t carry = 0;
+  for (int i = 0; i < kFixed; ++i) {
+    carry += (int64_t)a.w[i] + sign * (int64_t)((uint64_t)b.w[i] * times);
+    a.w[i] = (uint32_t)carry;
+    carry >>= 32;
+  }
+}
+
+bool below(const Fixed &a, const Fixed &b) {
+  for (int i = kFixed - 1; i >= 0; --i)
+    if (a.w[i] != b.w[i]) return a.w[i] < b.w[i];
+  return false;
+}
+
+// a += sign * times * arctan(1 / k), by its series in 1 / k
+void add_arctan(Fixed &a, uint32_t k, int sign, uint32_t times) {
+  Fixed power{};
+  power.w[kFixed - 1] = 1;
+  divide(power, k);
+  const Fixed zero{};
+  for (uint32_t n = 1; below(zero, power); n += 2, sign = -sign) {
+    Fixed term = power;
+    divide(term, n);
+    add(a, term, sign, times);
+    divide(power, k * k);
+  }
+}
+
+struct PerTurn {
+  uint32_t w[kTurnWords];
+  PerTurn() : w{} {
+    Fixed turn{}, rest{};  // 2 pi = 32 arctan(1/5) - 8 arctan(1/239) (Machin)
+    add_arctan(turn, 5, 1, 32);
+    add_arctan(turn, 239, -1, 8);
+    rest.w[kFixed - 1] = 1;
+    for (int bit = kTurnWords * 32 - 1; bit >= 0; --bit) {  // long division of 1
+      add(rest, Fixed(rest), 1, 1);
+      if (below(rest, turn)) continue;
+      add(rest, turn, -1, 1);
+      w[bit / 32] |= 1u << (bit % 32);
+    }
+  }
+};
+
+// x / (2 pi) modulo 1 as a 64-bit fraction, to nearest.
+uint64_t turns_of(double x) {
+  static const PerTurn per;
+  int e;
+  const uint64_t m = (uint64_t)ldexp(frexp(fabs(x), &e), 53);  // |x| = m 2^(e - 53)
+  uint32_t product[kTurnWords + 3] = {};  // m / (2 pi)
+  unsigned __int128 carry = 0;
+  for (int i = 0; i < kTurnWords + 3; ++i) {
+    if (i < kTurnWords) carry += (unsigned __int128)per.w[i] * m;
+    product[i] = (uint32_t)carry;
+    carry >>= 32;
+  }
+  // the fraction's bits begin at this one of the product (those of small numbers past its end)
+  const int at = kTurnWords * 32 - (e - 53) - 64;
+  auto bit = [&](int i) -> uint64_t { return i < (kTurnWords + 3) * 32 ? product[i / 32] >> (i % 32) & 1 : 0; };
+  uint64_t f = bit(at - 1);
+  for (int i = 0; i < 64; ++i) f += bit(at + i) << i;
+  return x < 0 ? 0 - f : f;
+}
+
 bool bad_align(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
 // Fills one tensor's part of the parameters; ATTN_OK, ATTN_ERR_ARG or ATTN_ERR_ALIGN.
@@ -177,10 +263,7 @@ int attn_rope_table(const double *inv_freq, const int *axis, int n, int axes, lo
     if (!isfinite(inv_freq[i]) || axis[i] < 0 || axis[i] >= axes) return ATTN_ERR_ARG;
   }
   for (int i = 0; i < n; ++i) {
-    const double turns = inv_freq[i] / 6.283185307179586476925;
-    const double part = turns - floor(turns);  // modulo one turn: positions are whole numbers
-    // part rounds to 1.0 for a negative turn below 2^-53: that is no turn
-    const unsigned long long f = part >= 1.0 ? 0ull : (unsigned long long)ldexp(part, 64);
+    const uint64_t f = attn::turns_of(inv_freq[i]);  // modulo one turn: positions are whole numbers
     memcpy(&table[2 * i], &f, sizeof(f));
     table[2 * i + 1] = axis[i];
   }

@@ -321,9 +321,9 @@ ATTN_API int attn_fwd_fp8(const void *q8, const void *k8, const void *vt8, const
  *     y1 = x1 cos(phi) - x2 sin(phi),   y2 = x2 cos(phi) + x1 sin(phi),
  * the pair being dims (i, i + rot/2), or (2i, 2i + 1) with adjacent = 1.  Dims
  * from rot on are copied.  backward = 1 turns by -phi, which maps the gradient
- * of the output to that of the input.  Angles are exact for every int32
- * position (64-bit fractions of a turn, see attn_rope_table), the rotation is
- * float32, the output is rounded once.
+ * of the output to that of the input.  Angles are within 2^-25 turns for every
+ * int32 position and every inv_freq (64-bit fractions of a turn, see
+ * attn_rope_table), the rotation is float32, the output is rounded once.
  *
  * q, k   device pointers, bf16; element (b, h, n, d) at b * strides[0] +
  *        h * strides[1] + n * strides[2] + d.  Strides are host arrays of three
@@ -343,9 +343,9 @@ ATTN_API int attn_fwd_fp8(const void *q8, const void *k8, const void *vt8, const
  * `stream`, one launch, no workspace; may be captured into a CUDA graph.
  *
  * attn_rope_table (host only) fills table[2 i] with inv_freq[i] / (2 pi)
- * modulo 1 as a 64-bit fraction and table[2 i + 1] with axis[i], for i < n <=
- * 512; inv_freq finite, 0 <= axis[i] < axes.  The caller copies it to the
- * device once.
+ * modulo 1 as a 64-bit fraction (rounded to nearest from the exact value) and
+ * table[2 i + 1] with axis[i], for i < n <= 512; inv_freq finite, 0 <= axis[i] <
+ * axes.  The caller copies it to the device once.
  */
 #define ATTN_ROPE_MAX_AXES 8
 ATTN_API int attn_rope_table(const double *inv_freq, const int *axis, int n, int axes, long long *table);
