@@ -79,7 +79,7 @@ __device__ __forceinline__ void block_scan(long long &a, long long &b, long long
   b = (warp ? pb : 0) + ib - b;
 }
 
-// The last r in [0, n) with sums[r] <= x (sums ascending, sums[0] = 0); of
+// The last r in [0, n) with sums[r] <= x (sums ascending, sums[0] <= x); of
 // equal sums the last, which is the request that is not empty.
 __device__ __forceinline__ int find_last(const int *sums, int n, int x) {
   int lo = 0, hi = n;
@@ -171,8 +171,9 @@ __global__ void __launch_bounds__(kMaxThreads) attn_pages_kernel(const PagesPara
     }
   }
   if constexpr (ASSIGN) {
-    // Four tokens a thread, each looked up by itself so that the four page
-    // loads overlap; 16-byte stores where the buffers allow them.
+    // Four tokens a thread, so that their four page loads overlap: the first
+    // one's request by a search, the others' from there; 16-byte stores where the
+    // buffers allow them.
     const bool wide = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15u) == 0;
     for (int64_t i0 = (int64_t)gt * 4; i0 < p.max_tokens; i0 += (int64_t)gn * 4) {
       int slot[4], pos[4];
@@ -184,7 +185,11 @@ __global__ void __launch_bounds__(kMaxThreads) attn_pages_kernel(const PagesPara
         pos[u] = 0;
         from[u] = nullptr;
         if (i < total) {
-          while (r + 1 < p.B && tok[r + 1] <= i) ++r;
+          // usually the same request or the next one; past a run of idle ones by a search
+          if (r + 1 < p.B && tok[r + 1] <= i) {
+            ++r;
+            if (r + 1 < p.B && tok[r + 1] <= i) r += find_last(tok + r, p.B - r, (int)i);
+          }
           pos[u] = len[r] + (int)(i - tok[r]);
           const int j = pos[u] >> p.shift, have = (int)(((int64_t)len[r] + p.P - 1) >> p.shift);
           // a page of this step comes from the stack: its table entry may not be written yet

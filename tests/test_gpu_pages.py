@@ -184,3 +184,45 @@ def test_assign_and_release_captured():
         assert np.array_equal(out["slots"].cpu().numpy(), a["slots"]) and out["info"].tolist() == a["info"]
         assert np.array_equal(table.cpu().numpy(), o_table) and np.array_equal(lens.cpu().numpy(), o_lens)
         assert np.array_equal(free.cpu().numpy(), o_free) and count.item() == o_count and rel["info"].tolist() == b["info"]
+
+
+@pytest.mark.parametrize("active", [[0, 4999], [4998, 4999], [0, 1, 2500, 2501, 4000], [7], [3, 1000, 1001, 1002, 4999], []])
+def test_few_active_requests_among_idle_ones(active):
+    # one to six tokens each, so that a thread's four tokens lie in requests far apart
+    B, P = 5000, 16
+    r = np.random.default_rng(len(active))
+    lens, new = r.integers(0, 40, B), np.zeros(B, dtype=np.int64)
+    new[active] = r.integers(1, 7, len(active))
+    table, free, count = _state(B, P, 4, lens, 50, seed=3)
+    most = int(new.sum()) + 3
+    want = S.pages_assign(table, lens, new, free, count, P, most)
+    dt = _dev(table)
+    got = attn_pages_assign(dt, _dev(lens), _dev(new), _dev(free), _dev([count]), P, most)
+    _same(got, want, dt, ("lens", "free_count", "cu", "slots", "positions"))
+
+
+def test_idle_requests_cost_no_walk():
+    # two active requests at the two ends of the largest batch take about the time of two that are neighbours
+    B, P = 16384, 16
+    times = []
+    for active in ([0, 1], [0, B - 1]):
+        new = np.zeros(B, dtype=np.int64)
+        new[active] = 2
+        args = (_dev(np.full((B, 1), -1)), _dev(np.zeros(B)), _dev(new), _dev(np.arange(8)), _dev([8]), P, 4)
+        out = attn_pages_assign(*args)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(10):
+                attn_pages_assign(*args, out=out)
+        best = float("inf")
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            g.replay()
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        times.append(best)
+        assert out["slots"].tolist() == [7 * P, 7 * P + 1, 6 * P, 6 * P + 1]
+    assert times[1] <= 2 * times[0], times
