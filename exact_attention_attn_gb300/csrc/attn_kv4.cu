@@ -206,15 +206,37 @@ template <typename S>
 __device__ __forceinline__ void find_item(const Kv4Params &p, Piece &pc) {
   __shared__ Place found;
   __shared__ int tiles;
+  __shared__ int64_t wsum[S::WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int item = (int)blockIdx.x / p.cluster, rank = (int)blockIdx.x % p.cluster;
+  // The warp whose requests have the item: the first where 32 lanes hold them all, else each warp has a range of them
+  // and they are counted first.
+  int64_t before = 0;
+  int r0 = 0, r1 = p.B;
+  bool here = warp == 0;
   if (tid == 0) tiles = 0;
-  __syncthreads();
-  if (warp == 0) {  // items before each request, 32 requests at a time
-    int64_t before = 0;
-    for (int base = 0; base < p.B && before <= item; base += 32) {
+  if (p.B > 32) {
+    const int per = ((p.B + S::THREADS - 1) / S::THREADS) * 32;
+    r0 = min(warp * per, p.B);
+    r1 = min(r0 + per, p.B);
+    int64_t mine = 0;
+#pragma unroll 4
+    for (int r = r0 + lane; r < r1; r += 32) mine += (int64_t)p.H * load_request<S>(p, r).rt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) wsum[warp] = mine;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < S::WARPS; ++w)
+      if (w < warp) before += wsum[w];
+    here = item >= before && item < before + mine;
+  } else {
+    __syncthreads();
+  }
+  if (here) {  // items before each request, 32 requests at a time
+    for (int base = r0; base < r1 && before <= item; base += 32) {
       Request q{};
-      if (base + lane < p.B) q = load_request<S>(p, base + lane);
+      if (base + lane < r1) q = load_request<S>(p, base + lane);
       const int64_t n = (int64_t)p.H * q.rt;
       int64_t inc = n;
 #pragma unroll
