@@ -427,6 +427,24 @@ struct Item {
   }
 };
 
+// The first request from r on that has query tokens (B if none): the first whose
+// end in cu, which does not descend here, lies past the end of request r - 1, by a
+// search of the warp in 32 parts.
+__device__ __noinline__ int next_active(const int *cu, int B, int T, int r) {
+  const int lane = threadIdx.x & 31, from = min(max(cu[r], 0), T);
+  int lo = r, hi = B;
+  while (lo < hi) {
+    const int step = (hi - lo + 31) >> 5, last = min(lo + (lane + 1) * step, hi) - 1;
+    const bool past = lo + lane * step < hi && min(max(cu[last + 1], 0), T) > from;
+    const unsigned parts = __ballot_sync(0xffffffffu, past);
+    if (parts == 0) return B;
+    lo += (__ffs(parts) - 1) * step;
+    if (step == 1) return lo;
+    hi = min(lo + step, hi);
+  }
+  return B;
+}
+
 struct Walk {
   int64_t begin;   // of the place, in the line
   int left;        // units of the piece from there on
@@ -443,9 +461,14 @@ struct Walk {
   template <typename S>
   __device__ __forceinline__ bool next(const Kv4Params &p, Item &it) {
     while (left > 0) {
-      while (at.h == p.H || q.rt == 0) {  // also steps over requests without query tokens
+      if (at.h == p.H) {
         if (++at.r >= p.B) return false;
         q = load_request<S>(p, at.r);
+        if (q.rt == 0) {
+          at.r = next_active(p.cu, p.B, p.T, at.r + 1);
+          if (at.r >= p.B) return false;
+          q = load_request<S>(p, at.r);
+        }
         at.h = at.rt = at.off = 0;
       }
       const int each = q.tiles + S::START, n = min(each - at.off, left);

@@ -85,11 +85,15 @@ def _time(call):
     return best / 10
 
 
-@pytest.mark.parametrize("width", [20, 3000])
-def test_idle_slots_cost_no_walk(width):
+@pytest.mark.parametrize("tokens", [300, 330])  # (330: the second item begins inside a warp's piece)
+@pytest.mark.parametrize("width", [25, 3000])
+def test_idle_slots_cost_no_walk(width, tokens):
     # two active slots at the ends of the largest batch: the lengths are read by all threads of a CTA, not by one warp
-    # (some 200 us) or, between an item and the next, by one load after the other
-    cache = _cache(64, 5)
-    batch, _ = _batch(16384, [0, 16383], [300, 300], [1, 1], width, 64, 6)
+    # (some 200 us) or, between an item and the next, by one load after the other (2.5 ms)
+    g = torch.Generator().manual_seed(5)
+    k = torch.randn((64 * P, 1, D), generator=g).to(torch.bfloat16).cuda()
+    cache = attn_kv4_cache(64, 1, D, P)
+    attn_kv4_append(k, k, _dev(range(64 * P)), cache, P)
+    batch, _ = _batch(16384, [0, 16383], [tokens, tokens], [1, 1], width, 64, 6)
     out, lse = attn_fwd_kv4(*batch, cache, P)
-    assert _time(lambda: attn_fwd_kv4(*batch, cache, P, out=out, lse=lse)) <= 0.1  # ms
+    assert _time(lambda: attn_fwd_kv4(*batch, cache, P, out=out, lse=lse)) <= 0.12  # ms
