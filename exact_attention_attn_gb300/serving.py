@@ -306,9 +306,12 @@ def attn_pages_assign(table, lens, new_lens, free_pages, free_count, page_size: 
     out["free_count"] free_count, for updates in place."""
     key = plan = None
     if out and len(out) == 6:
-        key = ("assign", page_size, max_tokens, _sig(table), _sig(lens), _sig(new_lens), _sig(free_pages),
-               _sig(free_count), *out, *map(_sig, out.values()))
-        plan = _plans.get(key)
+        try:
+            key = ("assign", page_size, max_tokens, _sig(table), _sig(lens), _sig(new_lens), _sig(free_pages),
+                   _sig(free_count), *out, *map(_sig, out.values()))
+            plan = _plans.get(key)
+        except AttributeError:  # (an output that is None: made below)
+            pass
     if plan:
         o = out
     else:

@@ -196,3 +196,20 @@ def test_binding_refuses_cpu_tensors_and_shapes(lib):  # noqa: F811
                  lambda: A.attn_pages_release(one[None], one, one, one, one, 16)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_outputs_given_as_none_are_made(monkeypatch):
+    # six entries, some of them None, as with fewer
+    import exact_attention_attn_gb300 as A
+    from exact_attention_attn_gb300 import serving
+    monkeypatch.setattr(serving, "_cuda", lambda *a, **k: None)
+    calls = []
+    monkeypatch.setattr(serving, "_run", lambda *a: calls.append(a))
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    names = ("lens", "free_count", "cu", "slots", "positions", "info")
+    for given in ({}, {n: None for n in names}, {**{n: None for n in names}, "slots": i32(5)}):
+        o = A.attn_pages_assign(i32(2, 3), i32(2), i32(2), i32(4), i32(1), 16, 5, out=given)
+        assert {n: tuple(o[n].shape) for n in names} == {"lens": (2,), "free_count": (1,), "cu": (3,), "slots": (5,),
+                                                         "positions": (5,), "info": (2,)}
+        assert given.get("slots") is None or o["slots"] is given["slots"]
+    assert len(calls) == 3
