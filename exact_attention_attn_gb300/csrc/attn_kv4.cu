@@ -28,11 +28,15 @@
 // Softmax.  p = 2^(y - ref), ref a per-row reference 10 above which the warp
 // rescales only when some y exceeds ref + 15; P s' is rounded to half
 // precision (2^-11 relative; bfloat16's 2^-8 would be as large as the output's own
-// rounding) times a power of two of the row's and group's own.  That follows the
-// largest scale s' which the row has seen, but never takes the row's products so
-// low that a rounding passes 2^-28 of their sum: a token that is hidden from the
-// row, or that it gives no weight, cannot take the others' bits, however large its
-// V is.  l and the sums of p m' are in float32.
+// rounding) times a power of two per group that brings the largest scale s' seen
+// below 1.  That keeps the products' roundings below 2^-28 of their sum while
+// scales lie within 2^6 of each other.  A warp that meets others (a token of huge
+// V which some rows do not see, or give no weight, would take the bits of the
+// rest) begins its item again in a second form of the loop, with a power of two
+// for each row and group that goes by the products the row really has: up to
+// twice the time (64 requests of 1 to 8192 tokens: 50 us; 58 with one such token a
+// request, 77 with one in a hundred).  Taking that form always cost 3 to 5 % of
+// every call.  l and the sums of p m' are in float32.
 //
 // Work split.  The tiles of all (request, kv head, row tile) items form one
 // line, cut into equal pieces, one per resident warp: lengths are read on the
@@ -67,6 +71,7 @@
 #include <string.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "attn.h"
 #include "attn_internal.h"
@@ -763,300 +768,405 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
 
     float acc[NT][G][4][4];  // O^T: [row tile][group][dim tile][c]
     float ref[NT][2], l[NT][2], vm[NT][G][2];
-    // the power of two that a row's weighted scales of V are brought to half precision by (0: a row that sees nothing
-    // here), and the rows' largest
-    float isig[NT][G][2], top_sig[G];
+    float isig[NT][G][2];  // the power of two by which a row's weighted scales of V are brought to half precision
     int lim[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        ref[nt][c] = kNoRef;
-        l[nt][c] = 0.f;
         const int row = row0 + nt * 8 + 2 * t + c;
         lim[nt][c] = row < rows ? it.limit(row, p) : 0;
+      }
+
+    // The item's tiles.  Usually V's scales lie within 2^6 of each other, and one power of two a group serves all rows
+    // (EACH false); where they do not, or a score passes 2^20, that ends with false, and the tiles are taken again with
+    // one for each row and group.
+    auto attend = [&](auto each) -> bool {
+      constexpr bool EACH = decltype(each)::value;
+      float top_sig[G];  // the rows' largest power of two
+      int least[G];      // exponent (biased by 127) of the smallest scale in the units that moved a reference
 #pragma unroll
-        for (int j = 0; j < G; ++j) isig[nt][j][c] = lim[nt][c] > it.tile0 * TK ? pow2(kMostSig) : 0.f;
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          ref[nt][c] = kNoRef;
+          l[nt][c] = 0.f;
+          // (0: a row that sees nothing here)
+#pragma unroll
+          for (int j = 0; j < G; ++j) isig[nt][j][c] = lim[nt][c] > it.tile0 * TK ? pow2(kMostSig) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          vm[nt][j][0] = vm[nt][j][1] = 0.f;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) acc[nt][j][d][0] = acc[nt][j][d][1] = acc[nt][j][d][2] = acc[nt][j][d][3] = 0.f;
+        }
       }
 #pragma unroll
       for (int j = 0; j < G; ++j) {
-        vm[nt][j][0] = vm[nt][j][1] = 0.f;
-#pragma unroll
-        for (int d = 0; d < 4; ++d) acc[nt][j][d][0] = acc[nt][j][d][1] = acc[nt][j][d][2] = acc[nt][j][d][3] = 0.f;
+        top_sig[j] = pow2(kMostSig);
+        least[j] = 255;
       }
-    }
-#pragma unroll
-    for (int j = 0; j < G; ++j) top_sig[j] = pow2(kMostSig);
 
-    for (int tile = it.tile0; tile < stop; ++tile) {
-      cp_async_wait<STAGES - 1>();
-      __syncwarp();
+      for (int tile = it.tile0; tile < stop; ++tile) {
+        cp_async_wait<STAGES - 1>();
+        __syncwarp();
 #pragma unroll 1
-      for (int u = 0; u < TK / 32; ++u) {
-        const int tok0 = tile * TK + u * 32;
-        if (u > 0 && tok0 >= it.q.len) break;
-        const bool edge = tok0 + 32 > full_to, tail = tok0 + 32 > it.q.len;
-        // the first K row of each 16 tokens; everything else is at a fixed distance
-        const uint32_t kc = ring_s + st * S::STAGE + u * (S::code_row(2, 0) - S::code_row(0, 0)) + row_off;
-        const uint32_t km = ring_s + st * S::STAGE + u * (S::pair_row(2, 0) - S::pair_row(0, 0)) + kv4_codes_bytes(G, P) +
-                            g * kKv4PairBytes;
-        // the lane's tokens of S^T: ta, ta + 8 of each 16
-        const int ta = tok0 + g;
+        for (int u = 0; u < TK / 32; ++u) {
+          const int tok0 = tile * TK + u * 32;
+          if (u > 0 && tok0 >= it.q.len) break;
+          const bool tail = tok0 + 32 > it.q.len;
+          bool edge = tok0 + 32 > full_to;
+          // the first K row of each 16 tokens; everything else is at a fixed distance
+          const uint32_t kc = ring_s + st * S::STAGE + u * (S::code_row(2, 0) - S::code_row(0, 0)) + row_off;
+          const uint32_t km = ring_s + st * S::STAGE + u * (S::pair_row(2, 0) - S::pair_row(0, 0)) +
+                              kv4_codes_bytes(G, P) + g * kKv4PairBytes;
+          // the lane's tokens of S^T: ta, ta + 8 of each 16
+          const int ta = tok0 + g;
 
-        // S^T = K Q^T on the codes, joined over the groups with scales and minima
-        float x[2][NT][4];
+          // S^T = K Q^T on the codes, joined over the groups with scales and minima
+          float x[2][NT][4];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
+          for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-          for (int j = 0; j < G; ++j) {
-            uint32_t w[4];  // tokens g and g + 8 of the first 32 dims, then of the others
-            ldmatrix4(w, kc + S::code_row(hf, j));
-            const uint32_t pa = lds32(km + S::pair_row(hf, j)), pb = lds32(km + S::pair_row(hf, j) + 8 * kKv4PairBytes);
-            float s[NT][4];
+            for (int j = 0; j < G; ++j) {
+              uint32_t w[4];  // tokens g and g + 8 of the first 32 dims, then of the others
+              ldmatrix4(w, kc + S::code_row(hf, j));
+              const uint32_t pa = lds32(km + S::pair_row(hf, j));
+              const uint32_t pb = lds32(km + S::pair_row(hf, j) + 8 * kKv4PairBytes);
+              float s[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+              for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t xa = w[2 * k], xb = w[2 * k + 1];
+              for (int k = 0; k < 2; ++k) {
+                uint32_t xa = w[2 * k], xb = w[2 * k + 1];
 #pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-                const uint32_t a0 = xa & 0x000f000fu, a1 = xb & 0x000f000fu;
-                const uint32_t a2 = xa & 0x00f000f0u, a3 = xb & 0x00f000f0u;
+                for (int hh = 0; hh < 2; ++hh) {
+                  const uint32_t a0 = xa & 0x000f000fu, a1 = xb & 0x000f000fu;
+                  const uint32_t a2 = xa & 0x00f000f0u, a3 = xb & 0x00f000f0u;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  mma_f16(s[nt], a0, a1, a2, a3, qb[nt][j][2 * k + hh][0], qb[nt][j][2 * k + hh][1]);
-                xa >>= 8;
-                xb >>= 8;
+                  for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(s[nt], a0, a1, a2, a3, qb[nt][j][2 * k + hh][0], qb[nt][j][2 * k + hh][1]);
+                  xa >>= 8;
+                  xb >>= 8;
+                }
               }
+              const float sa = __uint_as_float(pa << 16), ma = __uint_as_float(pa & 0xffff0000u);
+              const float sb = __uint_as_float(pb << 16), mb = __uint_as_float(pb & 0xffff0000u);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  float &xa = x[hf][nt][c], &xb = x[hf][nt][2 + c];
+                  xa = fmaf(sa, s[nt][c], j ? fmaf(ma, qsum[nt][j][c], xa) : ma * qsum[nt][j][c]);
+                  xb = fmaf(sb, s[nt][2 + c], j ? fmaf(mb, qsum[nt][j][c], xb) : mb * qsum[nt][j][c]);
+                }
             }
-            const float sa = __uint_as_float(pa << 16), ma = __uint_as_float(pa & 0xffff0000u);
-            const float sb = __uint_as_float(pb << 16), mb = __uint_as_float(pb & 0xffff0000u);
+          }
+          // V's scales and minima of the lane's tokens (of those past the request's end none, whatever they are)
+          uint32_t pv[2][G][2];
+          float big_v = 0.f;
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+              const uint32_t vp = km + kv4_side_bytes(G, P) + S::pair_row(hf, j);
+              pv[hf][j][0] = lds32(vp);
+              pv[hf][j][1] = lds32(vp + 8 * kKv4PairBytes);
+              if (tail) {
+                if (ta + hf * 16 >= it.q.len) pv[hf][j][0] = 0u;
+                if (ta + hf * 16 + 8 >= it.q.len) pv[hf][j][1] = 0u;
+              }
+              big_v = max3f(big_v, __uint_as_float(pv[hf][j][0] << 16) * top_sig[j],
+                            __uint_as_float(pv[hf][j][1] << 16) * top_sig[j]);
+            }
+          // e = y - ref in log2 units; hidden tokens -inf (selected, so that nothing they hold is used)
+          float e[2][NT][4];
+          float top = -INFINITY;
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                float &xa = x[hf][nt][c], &xb = x[hf][nt][2 + c];
-                xa = fmaf(sa, s[nt][c], j ? fmaf(ma, qsum[nt][j][c], xa) : ma * qsum[nt][j][c]);
-                xb = fmaf(sb, s[nt][2 + c], j ? fmaf(mb, qsum[nt][j][c], xb) : mb * qsum[nt][j][c]);
+                float &ea = e[hf][nt][c], &eb = e[hf][nt][2 + c];
+                ea = fmaf(x[hf][nt][c], fac[nt][c], -ref[nt][c]);
+                eb = fmaf(x[hf][nt][2 + c], fac[nt][c], -ref[nt][c]);
+                if (edge) {
+                  if (ta + hf * 16 >= lim[nt][c]) ea = -INFINITY;
+                  if (ta + hf * 16 + 8 >= lim[nt][c]) eb = -INFINITY;
+                }
+                top = max3f(top, ea, eb);
               }
-          }
-        }
-        // V's scales and minima of the lane's tokens (of those past the request's end none, whatever they are)
-        uint32_t pv[2][G][2];
-        float big_v = 0.f;
+          if (__any_sync(0xffffffffu, top > 15.f || big_v > 1.9f)) {  // move the references up
+            if constexpr (!EACH) {
+              // The largest scale becomes [0.5, 1), so that no weight up to 2^15 overflows.  A row's largest product
+              // is then at least 2^(kLeastTop - 1), if the smallest scale of the units that moved references is not
+              // below 2^-6 of the largest: the row's heaviest token (weight 2^10 then) was in one of them.
+              bool plain = true;
+              float fs[G];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-          for (int j = 0; j < G; ++j) {
-            const uint32_t vp = km + kv4_side_bytes(G, P) + S::pair_row(hf, j);
-            pv[hf][j][0] = lds32(vp);
-            pv[hf][j][1] = lds32(vp + 8 * kKv4PairBytes);
-            if (tail) {
-              if (ta + hf * 16 >= it.q.len) pv[hf][j][0] = 0u;
-              if (ta + hf * 16 + 8 >= it.q.len) pv[hf][j][1] = 0u;
-            }
-            big_v = max3f(big_v, __uint_as_float(pv[hf][j][0] << 16) * top_sig[j],
-                          __uint_as_float(pv[hf][j][1] << 16) * top_sig[j]);
-          }
-        // e = y - ref in log2 units; hidden tokens -inf (selected, so that nothing they hold is used)
-        float e[2][NT][4];
-        float top = -INFINITY;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float &ea = e[hf][nt][c], &eb = e[hf][nt][2 + c];
-              ea = fmaf(x[hf][nt][c], fac[nt][c], -ref[nt][c]);
-              eb = fmaf(x[hf][nt][2 + c], fac[nt][c], -ref[nt][c]);
-              if (edge) {
-                if (ta + hf * 16 >= lim[nt][c]) ea = -INFINITY;
-                if (ta + hf * 16 + 8 >= lim[nt][c]) eb = -INFINITY;
-              }
-              top = max3f(top, ea, eb);
-            }
-        if (__any_sync(0xffffffffu, top > 15.f || big_v > 1.9f)) {  // move the references up
-          // Exponents (biased by 127) of the scales that are numbers, in both halves of a word, and of the largest of a
-          // group; those of the rows' new powers of two
-          uint32_t es[G][2][2];
-          int big[G], most[G];
-#pragma unroll
-          for (int j = 0; j < G; ++j) {
-            big[j] = 0;
-            most[j] = -127;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const uint32_t s = pv[hf][j][u] << 16;
-                const int ex = s < 0x7f800000u ? s >> 23 : 0;
-                es[j][hf][u] = ex * 0x10001u;
-                big[j] = max(big[j], ex);
-              }
-            big[j] = __reduce_max_sync(0xffffffffu, big[j]);
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float down[2], f[2];
-            uint32_t ey[2][2][2];  // [half][token][row]: exponent of the token's weight, far down where it is hidden
-            int up[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float m = -INFINITY;
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int u = c; u < 4; u += 2)
-                  if (e[hf][nt][u] != -INFINITY) m = fmaxf(m, __fmul_rn(x[hf][nt][u], fac[nt][c]));
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-              const float now = fmaxf(ref[nt][c], m - 10.f);
-              down[c] = ref[nt][c] - now;
-              f[c] = ex2_approx(down[c]);
-              up[c] = (int)ceilf(fminf(-down[c], 300.f));  // whole powers of two that the weights have shrunk by
-              ref[nt][c] = now;
-              l[nt][c] *= f[c];
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int u = c; u < 4; u += 2)
-                  if (e[hf][nt][u] != -INFINITY) e[hf][nt][u] = fmaf(x[hf][nt][u], fac[nt][c], -now);
-              if (__any_sync(0xffffffffu, now > kNoRef && fabsf(now) >= 0x1p20f)) {
-                // The rounding of the product that gave the reference counts here: without it the largest score's y may
-                // be anything instead of 10, and its weight none or infinite.
+              for (int j = 0; j < G; ++j) {
+                int big = 0;  // of the scales that are numbers
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-                  for (int u = c; u < 4; u += 2) {
-                    const float y = __fsub_rn(__fmul_rn(x[hf][nt][u], fac[nt][c]), now);
-                    if (e[hf][nt][u] != -INFINITY) e[hf][nt][u] = y > 15.f ? 15.f : y;
+                  for (int u = 0; u < 2; ++u) {
+                    const uint32_t s = pv[hf][j][u] << 16;
+                    const int ex = s < 0x7f800000u ? s >> 23 : 0;
+                    big = max(big, ex);
+                    if (!tail || ta + hf * 16 + u * 8 < it.q.len) least[j] = min(least[j], ex);
                   }
+                big = __reduce_max_sync(0xffffffffu, big);
+                least[j] = __reduce_min_sync(0xffffffffu, least[j]);
+                const int old = exp_of(top_sig[j]), now = min(old, 126 - big);
+                plain = plain && least[j] + now >= 127 - 11 + kLeastTop;
+                top_sig[j] = pow2(now);
+                fs[j] = pow2(max(now - old, -126));  // (from its first value there is nothing to take along)
               }
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                  const float y = e[hf][nt][2 * u + c];
-                  const bool seen = y != -INFINITY;
-                  // (the bits of 1.5 * 2^23 + y are those of 1.5 * 2^23, plus y's nearest whole number)
-                  const uint32_t whole = __float_as_uint(fminf(fmaxf(y, -1000.f), 100.f) + 12582912.f) - 0x4b400000u;
-                  ey[hf][u][c] = seen ? whole + kBias : kBias - 2000u;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < G; ++j) {
-              // The exponent of the largest weighted scale that each row sees here (row c in half c), or of what it has
-              // summed so far over the largest code.
-              uint32_t key = 0;
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                float held = 0.f;
-#pragma unroll
-                for (int d = 0; d < 4; ++d) held = max3f(held, acc[nt][j][d][c], acc[nt][j][d][2 + c]);
-                key |= (uint32_t)(exp_of(held) + 127 + 20 - exp_of(isig[nt][j][c]) - up[c] + (int)kBias) << (16 * c);
-              }
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) key = __vmaxu2(key, es[j][hf][u] + ey[hf][u][0] + (ey[hf][u][1] << 16));
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) key = __vmaxu2(key, __shfl_xor_sync(0xffffffffu, key, o));
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                vm[nt][j][c] *= f[c];
-                // The largest scale becomes [0.5, 1), so that no weight up to 2^15 overflows, unless that took the
-                // row's largest product too low; what the row has summed keeps its place where that falls.
-                const int old = exp_of(isig[nt][j][c]);
-                const int low = min(old, 126 - big[j]);
-                const int need = kLeastTop + 127 + (int)kBias - (int)(c ? key >> 16 : key & 0xffffu);
-                const int next = old == -127 ? old : max(-126, min(min(old + up[c], kMostSig), max(low, need)));
-                const float by =
-                    next <= old ? f[c] * pow2(max(next - old, -126)) : ex2_approx(down[c] + (float)(next - old));
-                isig[nt][j][c] = pow2(next);
-                most[j] = max(most[j], next);
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                  acc[nt][j][d][c] *= by;
-                  acc[nt][j][d][2 + c] *= by;
-                }
-              }
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < G; ++j) top_sig[j] = pow2(__reduce_max_sync(0xffffffffu, most[j]));
-        }
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float pr[NT][4], pm[NT][4];  // weights, and what multiplies the minima
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              pr[nt][c] = ex2_approx(e[hf][nt][c]);
-              pr[nt][2 + c] = ex2_approx(e[hf][nt][2 + c]);
-              l[nt][c] += pr[nt][c] + pr[nt][2 + c];
-              pm[nt][c] = pr[nt][c] * kDown;
-              pm[nt][2 + c] = pr[nt][2 + c] * kDown;
-            }
-          // O^T += V^T P^T
-#pragma unroll
-          for (int j = 0; j < G; ++j) {
-            const uint32_t pa = pv[hf][j][0], pb = pv[hf][j][1];
-            const float sa = __uint_as_float(pa << 16), sb = __uint_as_float(pb << 16);
-            const float ma = __uint_as_float(pa & 0xffff0000u), mb = __uint_as_float(pb & 0xffff0000u);
-            uint32_t b0[NT], b1[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float w[4];
-              const uint64_t up = f2_pack(isig[nt][j][0], isig[nt][j][1]);
-              f2_unpack(f2_mul(f2_pack(pr[nt][0], pr[nt][1]), f2_mul(f2_pack(sa, sa), up)), w[0], w[1]);
-              f2_unpack(f2_mul(f2_pack(pr[nt][2], pr[nt][3]), f2_mul(f2_pack(sb, sb), up)), w[2], w[3]);
-              if (!edge) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) vm[nt][j][c] = fmaf(pm[nt][2 + c], mb, fmaf(pm[nt][c], ma, vm[nt][j][c]));
-              } else {  // a hidden token's scale and minimum may be anything
+              for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                  const bool no_a = e[hf][nt][c] == -INFINITY, no_b = e[hf][nt][2 + c] == -INFINITY;
-                  if (no_a) w[c] = 0.f;
-                  if (no_b) w[2 + c] = 0.f;
-                  vm[nt][j][c] = fmaf(pm[nt][2 + c], no_b ? 0.f : mb, fmaf(pm[nt][c], no_a ? 0.f : ma, vm[nt][j][c]));
+                  float m = -INFINITY;
+#pragma unroll
+                  for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int u = c; u < 4; u += 2)
+                      if (e[hf][nt][u] != -INFINITY) m = fmaxf(m, x[hf][nt][u] * fac[nt][c]);
+#pragma unroll
+                  for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                  const float now = fmaxf(ref[nt][c], m - 10.f);
+                  const float f = ex2_approx(ref[nt][c] - now);
+                  plain = plain && (now <= kNoRef || fabsf(now) < 0x1p20f);
+                  ref[nt][c] = now;
+#pragma unroll
+                  for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int u = c; u < 4; u += 2)
+                      if (e[hf][nt][u] != -INFINITY) e[hf][nt][u] = fmaf(x[hf][nt][u], fac[nt][c], -now);
+                  l[nt][c] *= f;
+#pragma unroll
+                  for (int j = 0; j < G; ++j) {
+                    vm[nt][j][c] *= f;
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                      acc[nt][j][d][c] *= f * fs[j];
+                      acc[nt][j][d][2 + c] *= f * fs[j];
+                    }
+                  }
+                }
+              if (!__all_sync(0xffffffffu, plain)) return false;
+            } else {
+              // Exponents (biased by 127) of the scales that are numbers, in both halves of a word, and of the largest
+              // of a group; those of the rows' new powers of two
+              uint32_t es[G][2][2];
+              int big[G], most[G];
+              bool far_off = false;  // a scale times the power of two may pass float32, at a token of next to no weight
+#pragma unroll
+              for (int j = 0; j < G; ++j) {
+                big[j] = 0;
+                most[j] = -127;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                  for (int u = 0; u < 2; ++u) {
+                    const uint32_t s = pv[hf][j][u] << 16;
+                    const int ex = s < 0x7f800000u ? s >> 23 : 0;
+                    es[j][hf][u] = ex * 0x10001u;
+                    big[j] = max(big[j], ex);
+                  }
+                big[j] = __reduce_max_sync(0xffffffffu, big[j]);
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float down[2], f[2];
+                uint32_t ey[2][2][2];  // [half][token][row]: the weight's exponent, far down where the token is hidden
+                int up[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  float m = -INFINITY;
+#pragma unroll
+                  for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int u = c; u < 4; u += 2)
+                      if (e[hf][nt][u] != -INFINITY) m = fmaxf(m, __fmul_rn(x[hf][nt][u], fac[nt][c]));
+#pragma unroll
+                  for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                  const float now = fmaxf(ref[nt][c], m - 10.f);
+                  down[c] = ref[nt][c] - now;
+                  f[c] = ex2_approx(down[c]);
+                  up[c] = (int)ceilf(fminf(-down[c], 300.f));  // whole powers of two that the weights have shrunk by
+                  ref[nt][c] = now;
+                  l[nt][c] *= f[c];
+#pragma unroll
+                  for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int u = c; u < 4; u += 2)
+                      if (e[hf][nt][u] != -INFINITY) e[hf][nt][u] = fmaf(x[hf][nt][u], fac[nt][c], -now);
+                  if (__any_sync(0xffffffffu, now > kNoRef && fabsf(now) >= 0x1p20f)) {
+                    // The rounding of the product that gave the reference counts here: without it the largest score's
+                    // y may be anything instead of 10, and its weight none or infinite.
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                      for (int u = c; u < 4; u += 2) {
+                        const float y = __fsub_rn(__fmul_rn(x[hf][nt][u], fac[nt][c]), now);
+                        if (e[hf][nt][u] != -INFINITY) e[hf][nt][u] = y > 15.f ? 15.f : y;
+                      }
+                  }
+#pragma unroll
+                  for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                      const float y = e[hf][nt][2 * u + c];
+                      const bool seen = y != -INFINITY;
+                      // (the bits of 1.5 * 2^23 + y are those of 1.5 * 2^23, plus y's nearest whole number)
+                      const float near = fminf(fmaxf(y, -1000.f), 100.f);
+                      ey[hf][u][c] = seen ? __float_as_uint(near + 12582912.f) - 0x4b400000u + kBias : kBias - 2000u;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                  // The exponent of the largest weighted scale that each row sees here (row c in half c), or of what it
+                  // has summed so far over the largest code.
+                  uint32_t key = 0;
+#pragma unroll
+                  for (int c = 0; c < 2; ++c) {
+                    float held = 0.f;
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) held = max3f(held, acc[nt][j][d][c], acc[nt][j][d][2 + c]);
+                    const int sum = exp_of(held) + 20 - exp_of(isig[nt][j][c]) - up[c];
+                    key |= (uint32_t)(sum + 127 + (int)kBias) << (16 * c);
+                  }
+#pragma unroll
+                  for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) key = __vmaxu2(key, es[j][hf][u] + ey[hf][u][0] + (ey[hf][u][1] << 16));
+#pragma unroll
+                  for (int o = 4; o < 32; o <<= 1) key = __vmaxu2(key, __shfl_xor_sync(0xffffffffu, key, o));
+#pragma unroll
+                  for (int c = 0; c < 2; ++c) {
+                    vm[nt][j][c] *= f[c];
+                    // The largest scale becomes [0.5, 1), so that no weight up to 2^15 overflows, unless that took the
+                    // row's largest product too low; what the row has summed keeps its place where that falls.
+                    const int old = exp_of(isig[nt][j][c]);
+                    const int low = min(old, 126 - big[j]);
+                    const int need = kLeastTop + 127 + (int)kBias - (int)(c ? key >> 16 : key & 0xffffu);
+                    const int next = old == -127 ? old : max(-126, min(min(old + up[c], kMostSig), max(low, need)));
+                    const float by =
+                        next <= old ? f[c] * pow2(max(next - old, -126)) : ex2_approx(down[c] + (float)(next - old));
+                    isig[nt][j][c] = pow2(next);
+                    most[j] = max(most[j], next);
+                    far_off = far_off || next > 252 - big[j];
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                      acc[nt][j][d][c] *= by;
+                      acc[nt][j][d][2 + c] *= by;
+                    }
+                  }
                 }
               }
-              b0[nt] = transpose8x8(half2_bits(w[0], w[1]));
-              b1[nt] = transpose8x8(half2_bits(w[2], w[3]));
+#pragma unroll
+              for (int j = 0; j < G; ++j) top_sig[j] = pow2(__reduce_max_sync(0xffffffffu, most[j]));
+              if (__any_sync(0xffffffffu, far_off)) edge = true;
             }
-            // dims 4g .. 4g + 3 of tokens (2t, 2t + 1) and (8 + 2t, 9 + 2t), then those of the other 32 dims
-            uint32_t z[4];
-            ldmatrix4_trans(z, kc + kv4_side_bytes(G, P) + S::code_row(hf, j));
+          }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t z0 = z[2 * k], z1 = z[2 * k + 1];
+          for (int hf = 0; hf < 2; ++hf) {
+            float pr[NT][4], pm[NT][4];  // weights, and what multiplies the minima
 #pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-                const uint32_t a0 = z0 & 0x000f000fu, a1 = z0 & 0x00f000f0u;
-                const uint32_t a2 = z1 & 0x000f000fu, a3 = z1 & 0x00f000f0u;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][j][2 * k + hh], a0, a1, a2, a3, b0[nt], b1[nt]);
-                z0 >>= 8;
-                z1 >>= 8;
+              for (int c = 0; c < 2; ++c) {
+                pr[nt][c] = ex2_approx(e[hf][nt][c]);
+                pr[nt][2 + c] = ex2_approx(e[hf][nt][2 + c]);
+                l[nt][c] += pr[nt][c] + pr[nt][2 + c];
+                pm[nt][c] = pr[nt][c] * kDown;
+                pm[nt][2 + c] = pr[nt][2 + c] * kDown;
+              }
+            // O^T += V^T P^T
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+              const uint32_t pa = pv[hf][j][0], pb = pv[hf][j][1];
+              const float sa = __uint_as_float(pa << 16), sb = __uint_as_float(pb << 16);
+              const float ma = __uint_as_float(pa & 0xffff0000u), mb = __uint_as_float(pb & 0xffff0000u);
+              uint32_t b0[NT], b1[NT];
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float w[4];
+                if constexpr (EACH) {
+                  const uint64_t up = f2_pack(isig[nt][j][0], isig[nt][j][1]);
+                  f2_unpack(f2_mul(f2_pack(pr[nt][0], pr[nt][1]), f2_mul(f2_pack(sa, sa), up)), w[0], w[1]);
+                  f2_unpack(f2_mul(f2_pack(pr[nt][2], pr[nt][3]), f2_mul(f2_pack(sb, sb), up)), w[2], w[3]);
+                } else {
+                  const float ua = sa * top_sig[j], ub = sb * top_sig[j];
+                  w[0] = pr[nt][0] * ua;
+                  w[1] = pr[nt][1] * ua;
+                  w[2] = pr[nt][2] * ub;
+                  w[3] = pr[nt][3] * ub;
+                }
+                if (!edge) {
+#pragma unroll
+                  for (int c = 0; c < 2; ++c) vm[nt][j][c] = fmaf(pm[nt][2 + c], mb, fmaf(pm[nt][c], ma, vm[nt][j][c]));
+                } else {
+                  // A hidden token's scale and minimum may be anything; a scale of next to no weight may have passed
+                  // float32 (of a weight above 2^-120 it has not: the row's products are below 2^6).
+#pragma unroll
+                  for (int c = 0; c < 2; ++c) {
+                    const bool no_a = e[hf][nt][c] == -INFINITY, no_b = e[hf][nt][2 + c] == -INFINITY;
+                    if (no_a || (EACH && e[hf][nt][c] < -120.f && sa < INFINITY)) w[c] = 0.f;
+                    if (no_b || (EACH && e[hf][nt][2 + c] < -120.f && sb < INFINITY)) w[2 + c] = 0.f;
+                    vm[nt][j][c] = fmaf(pm[nt][2 + c], no_b ? 0.f : mb, fmaf(pm[nt][c], no_a ? 0.f : ma, vm[nt][j][c]));
+                  }
+                }
+                b0[nt] = transpose8x8(half2_bits(w[0], w[1]));
+                b1[nt] = transpose8x8(half2_bits(w[2], w[3]));
+              }
+              // dims 4g .. 4g + 3 of tokens (2t, 2t + 1) and (8 + 2t, 9 + 2t), then those of the other 32 dims
+              uint32_t z[4];
+              ldmatrix4_trans(z, kc + kv4_side_bytes(G, P) + S::code_row(hf, j));
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                uint32_t z0 = z[2 * k], z1 = z[2 * k + 1];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                  const uint32_t a0 = z0 & 0x000f000fu, a1 = z0 & 0x00f000f0u;
+                  const uint32_t a2 = z1 & 0x000f000fu, a3 = z1 & 0x00f000f0u;
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][j][2 * k + hh], a0, a1, a2, a3, b0[nt], b1[nt]);
+                  z0 >>= 8;
+                  z1 >>= 8;
+                }
               }
             }
           }
         }
-      }
-      __syncwarp();  // every lane has read the stage
-      if (asked < stop) {
-        if (asked * S::PAGES - first >= 32) {
-          first += 32;
-          ids = ids_next;
-          ids_next = load_ids(p, it.r, first + 32, pages, lane);
+        __syncwarp();  // every lane has read the stage
+        if (asked < stop) {
+          if (asked * S::PAGES - first >= 32) {
+            first += 32;
+            ids = ids_next;
+            ids_next = load_ids(p, it.r, first + 32, pages, lane);
+          }
+          copy_tile<S>(head, page_row, asked++, ids, first, ring_s + st * S::STAGE, lane);
         }
-        copy_tile<S>(head, page_row, asked++, ids, first, ring_s + st * S::STAGE, lane);
+        cp_async_commit();
+        if (++st == STAGES) st = 0;
       }
-      cp_async_commit();
-      if (++st == STAGES) st = 0;
+      if constexpr (!EACH) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < G; ++j) isig[nt][j][0] = isig[nt][j][1] = top_sig[j];
+      }
+      return true;
+    };
+    if (!attend(std::false_type{})) {
+      cp_async_wait<0>();  // the copies that are on their way land before their stages are filled again
+      __syncwarp();
+      begin_copies();
+      attend(std::true_type{});
     }
 
     // ---- the item's end: the next item's first tiles are asked for, then the lanes are summed and the rows written

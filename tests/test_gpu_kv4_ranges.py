@@ -221,3 +221,27 @@ def test_scores_past_float32s_whole_numbers(D, P, power, wide):
         # V's own codes: within half a scale, and bfloat16's half step
         near = (out[0, :2].float().cpu() - v[at].to(torch.bfloat16).float()).abs()
         assert (near <= 0.55 * (v[at].max() - v[at].min()) / 15 + 0.02).all()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 16), (256, 64)])
+def test_all_weight_on_tokens_without_a_scale(D, P, wide):
+    # constant V (scale 0) has all the weight; the others' weights are 0 in float32, or nearly, however large their V is
+    n = 100
+    for low in (-150.0, -85.0, -40.0):
+        scores = torch.where(torch.arange(n) % 3 == 0, 0.0, low)
+        for power in (0, 20, 100):
+            v = _randn((n, 1, D), 28) * 2.0 ** power
+            v[::3] = 0.75
+            _run(_scored(scores, 1, D, 29), v, torch.ones((2, 4, D)), P, wide)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_scales_that_spread_late(wide):
+    # an item whose last tokens are the first to differ by more than 2^6: begun again, from tiles that were copied before
+    for n, at in ((1000, 999), (1000, 500), (2500, 2400)):
+        v = _randn((n, 2, 128), 30)
+        v[at] *= 2.0 ** 9
+        v[at - 1] *= 2.0 ** -30
+        out = _run(_randn((n, 2, 128), 31), v, _randn((2, 8, 128), 32), 16, wide)
+        assert torch.equal(out, _run(_randn((n, 2, 128), 31), v, _randn((2, 8, 128), 32), 16, wide))
