@@ -43,7 +43,7 @@
 // device, and no warp has more than another but for a tile.  An item's
 // beginning and end cost a warp about as much as START tiles, so each item is
 // START units longer than its tiles in that line (64 requests of 1 to 8192
-// tokens: 49.7 us with 4, 53.9 with 2, 67 with 1).  A warp works alone -- it
+// tokens: 49.4 us with 4, 55.4 with 2, 62.0 with 1).  A warp works alone -- it
 // copies its own tiles, keeps its own softmax and writes its own result -- so
 // that the latencies of an SM's warps overlap and short requests cost no
 // barrier.  An item cut by a piece's border leaves partial (ref, l, O) in a
@@ -53,18 +53,18 @@
 // Where the items are few and short by the sizes alone (no more than SMs, a few
 // tiles a warp), each has a cluster of 1 to 8 CTAs, whose parts are merged
 // through distributed shared memory, and there is no workspace and no second
-// kernel: one request of 129 tokens 6.4 us against 9.8, 8 requests of 1000 9.9
-// against 14.2, 4 of 4000 12.8 against 16.4.
+// kernel: one request of 129 tokens 7.1 us against 9.2, 8 requests of 1000 10.1
+// against 14.1, 4 of 4000 12.9 against 16.4.
 //
 // Memory.  Each warp owns a ring of stages of one tile (whole pages, 16 bytes
 // a lane and copy), and asks for the next tile as soon as a stage is read.
 //
-// Bound.  Beyond the first 16 us or so of a call the kernel runs at the copy
-// rate of HBM (Hq 32, Hkv 8, D 128: 228 requests of 1024 tokens to 2048, 269 MB
-// more, cost 39.5 us more: 6.8 TB/s); a call's beginning (finding the piece, the
-// first pages, Q), the items' ends and the merge are latency, which is what is
-// left in calls of 100 to 200 MB: 64 requests of 1 to 8192 tokens 4.1 TB/s, one
-// of 131072 3.8 TB/s.
+// Bound.  More tokens cost what HBM takes to copy them (Hq 32, Hkv 8, D 128: 228
+// requests of 1024 tokens to 2048, 269 MB more, cost 40.0 us more: 6.7 TB/s); a
+// call's beginning (finding the piece, the first pages, Q), the items' ends and
+// the merge are latency: 16 us in those calls, 19 us over the bytes' time in 64
+// requests of 1 to 8192 tokens (49.4 us, 4.2 TB/s), 17.5 us in one of 131072
+// (39.8 us, 3.8 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -1550,14 +1550,14 @@ int launch_kv4(Kv4Params &p, int device, int sms, cudaStream_t st) {
   if (items > ((int64_t)1 << 40) / (tiles + S::START)) return ATTN_ERR_ARG;  // a piece's units are 32-bit
   // Few and short items have a cluster of CTAs each: the most (a power of two up
   // to 8) that leaves each warp a tile and all clusters resident at once (a second
-  // wave costs more than it gives: 32 items of 2000 tokens 10.3 us in clusters of
-  // 4, 28.1 of 8), and no second kernel.  Pieces would have each warp's tiles done
+  // wave costs more than it gives: 32 items of 2000 tokens 10.4 us in clusters of
+  // 4, 28.0 of 8), and no second kernel.  Pieces would have each warp's tiles done
   // by all SMs, but cost about two tiles' time more.  Against pieces (D 128, 8 kv
-  // heads): 1 request of 2000 tokens 9.8 us against 13.2, of 8000 13.3 against
-  // 14.1, of 16000 (5 tiles a warp, 64 of 152 SMs) 17.2 against 16.5, 4 of 4000 12.8
-  // against 16.4, 8 of 2000 12.4 against 16.5, 16 of 2000 15.7 against 19.8.  Above 8
+  // heads): 1 request of 2000 tokens 10.1 us against 13.4, of 8000 13.4 against
+  // 14.2, of 16000 (5 tiles a warp, 64 of 152 SMs) 16.9 against 16.7, 4 of 4000 12.9
+  // against 16.4, 8 of 2000 12.6 against 16.4, 16 of 2000 15.4 against 19.5.  Above 8
   // tiles a warp, shorter requests' warps wait for the longest: 16 of 4000 and
-  // less 21.8 against 18.6.
+  // less 20.9 against 18.0.
   p.cluster = 1;
   for (int i = 0; i < kClusterSizes && tiles > S::WARPS * p.cluster && items <= held[i]; ++i) p.cluster *= 2;
   const int64_t ctas = items * p.cluster, warps = S::WARPS * p.cluster;  // of all items, of one item
@@ -1656,11 +1656,12 @@ int attn_fwd_kv4(const void *q, long long q_stride_t, long long q_stride_h, cons
   p.scale_log2 = scale * kLog2e;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // 16 rows a tile where the requests have more than 64 on average: K and V are
-  // then unpacked once for 16 rows.  With 112 rows (16 heads, 7 tokens, D 64,
-  // 4 requests up to 16384) 33.3 us against 38.2 in tiles of 8, with 256 rows
-  // (2 requests of 8192) 90 against 105; with 64 rows 39.2 against 37.8, with 16
-  // rows 32.6 against 31.3 (fewer warps an SM).  At D > 128 the accumulators of
-  // 16 rows do not fit the registers.
+  // then unpacked once for 16 rows.  With 16 heads on each of 4 kv heads: 112 rows
+  // (7 tokens, D 64, 4 requests up to 16384) 35.7 us against 39.0 in tiles of 8,
+  // 256 rows (D 64, 2 requests of 8192) 37.9 against 40.2, 112 rows at D 128 (51
+  // requests of 4096) 240 against 274; 64 rows (D 128, 4 requests of 8192) 37.3
+  // against 38.5, 16 rows (32 requests up to 4096) 24.1 against 23.4 (fewer warps
+  // an SM).  At D > 128 the accumulators of 16 rows do not fit the registers.
   const bool wide = (int64_t)p.group * ((T + B - 1) / B) > 64;
   switch (page_size) {
     case 16: return launch_page_size<16>(p, D / 64, wide, device, sms, st);

@@ -15,10 +15,13 @@
 // integers from L2 -- and reaches the same verdict, so no CTA waits for
 // another's sums and no workspace is kept; one cluster barrier separates the
 // reads of the state from its update, which makes updates in place safe.
-// Latency bound: the scan, then one search in shared memory per four tokens (a
-// decode step of 64 requests 4.6 us from a graph, 512 prompts of 44 Ki tokens
-// 9.8 us on 8 SMs, 12.0 with CTAs of 512 threads, 8.1 with clusters of 16, which
-// not every device grants: below the 11 us that the host's call takes anyway).
+// Latency bound: the scan, then a search in shared memory per four tokens, and
+// one more past each run of idle requests between them (a decode step of 64
+// requests 4.6 us from a graph, 512 slots of which two are active 5.5, 16384 of
+// them 26; 512 prompts of 44 Ki tokens 9.8 us on 8 SMs, 12.0 with CTAs of 512
+// threads, 8.1 with clusters of 16, which not every device grants: below the 11 us
+// that the host's call takes anyway; release of 16384 pages of 64 requests 31 us,
+// of 512 requests 15.5).
 #include <stdint.h>
 #include <string.h>
 

@@ -468,8 +468,10 @@ ATTN_API int attn_kv4_read(const void *cache, int num_pages, const int *slots, v
  *        probability times V's scale is rounded to 11 bits before the second
  *        product (to 2^-28 of the row's sum of these over its keys, where that
  *        is coarser), O once to bf16.
- *        Ranges: |q| scale up to 2^116; K and V up to 2^126, V times lens[r] up
- *        to 2^136 (float32 sums of weighted values, before their division).
+ *        Ranges: |q| scale up to 2^116, a value of q below 2^-25 of its row's
+ *        largest rounded to 2^-35 of that; K and V up to 2^126, V times lens[r]
+ *        up to 2^136 (float32 sums of weighted values, before their division);
+ *        a weight below 2^-110 of the row's largest may count as none.
  * Made for few query rows (query tokens x Hq / Hkv up to about 64 a request).
  * More work as well, at about 200 TFLOP/s; a long prompt chunk over a cached
  * prefix is better served by attn_kv4_read and attn_fwd.
