@@ -919,7 +919,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv4_kernel(const Kv4Params
                   }
                 big = __reduce_max_sync(0xffffffffu, big);
                 least[j] = __reduce_min_sync(0xffffffffu, least[j]);
-                const int old = exp_of(top_sig[j]), now = min(old, 126 - big);
+                const int old = exp_of(top_sig[j]), now = max(-126, min(old, 126 - big));
                 plain = plain && least[j] + now >= 127 - 11 + kLeastTop;
                 top_sig[j] = pow2(now);
                 fs[j] = pow2(max(now - old, -126));  // (from its first value there is nothing to take along)

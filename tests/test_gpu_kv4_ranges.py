@@ -245,3 +245,23 @@ def test_scales_that_spread_late(wide):
         v[at - 1] *= 2.0 ** -30
         out = _run(_randn((n, 2, 128), 31), v, _randn((2, 8, 128), 32), 16, wide)
         assert torch.equal(out, _run(_randn((n, 2, 128), 31), v, _randn((2, 8, 128), 32), 16, wide))
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 64)])
+def test_a_cache_made_by_hand_with_the_largest_scales(D, P, wide):
+    # scales of 2^126 with codes 0 and 1: more than quantising gives, within what the layout and the ranges allow
+    n, G = 50, D // 64
+    pages = -(-n // P)
+    cache = attn_kv4_cache(pages, 1, D, P)
+    k = _randn((n, 1, D), 33).to(torch.bfloat16).cuda()
+    attn_kv4_append(k, k, _dev(range(n)), cache, P)
+    cache[:, :, 36 * G * P:68 * G * P] &= 0x11
+    pairs = cache[:, :, 68 * G * P:].clone().view(torch.int16).view(pages, 1, G * P, 2)
+    pairs[..., 0], pairs[..., 1] = 0x7E80, 0
+    cache[:, :, 68 * G * P:] = pairs.view(torch.uint8).view(pages, 1, 4 * G * P)
+    q = _randn((3, 4, D), 34).to(torch.bfloat16).cuda()
+    table = _dev([list(range(pages)) + [-1] * (80000 // P if wide else 0)])
+    out, lse = attn_fwd_kv4(q, _dev([0, 3]), _dev([n]), table, cache, P)
+    assert attn_fwd_status() == 0 and torch.isfinite(out).all() and out.max() > 2.0 ** 122
+    _check(out, lse, q, n, cache, D, P)
