@@ -123,8 +123,8 @@ def _last_dim(t, name):
 
 
 def _written(strides, shape, name):
-    """A tensor that is written must not hold an element twice (an expanded dim)."""
-    if 0 in strides and any(n > 1 and x == 0 for n, x in zip(shape, strides)):
+    """A tensor that is written must not hold an element twice (an expanded dim; one without elements holds none)."""
+    if 0 in strides and 0 not in shape and any(n > 1 and x == 0 for n, x in zip(shape, strides)):
         raise ValueError(f"{name} is written and must not be expanded")
 
 

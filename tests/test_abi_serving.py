@@ -213,3 +213,22 @@ def test_outputs_given_as_none_are_made(monkeypatch):
                                                          "positions": (5,), "info": (2,)}
         assert given.get("slots") is None or o["slots"] is given["slots"]
     assert len(calls) == 3
+
+
+def test_a_table_without_columns_is_no_expanded_one(monkeypatch):
+    # a tensor without elements may have any strides (those made from an empty array are 0)
+    import numpy as np
+
+    import exact_attention_attn_gb300 as A
+    from exact_attention_attn_gb300 import serving
+    monkeypatch.setattr(serving, "_cuda", lambda *a, **k: None)
+    calls = []
+    monkeypatch.setattr(serving, "_run", lambda *a: calls.append(a))
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    table = torch.tensor(np.zeros((5, 0)), dtype=torch.int32)
+    assert table.stride(0) == 0
+    A.attn_pages_assign(table, i32(5), i32(5), i32(4), i32(1), 16, 0)
+    A.attn_pages_release(table, i32(5), i32(5), i32(4), i32(1), 16)
+    with pytest.raises(ValueError, match="expanded"):
+        A.attn_pages_assign(i32(1, 3).expand(5, 3), i32(5), i32(5), i32(4), i32(1), 16, 0)
+    assert len(calls) == 2
