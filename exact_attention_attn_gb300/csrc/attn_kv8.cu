@@ -908,7 +908,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv8_kernel(const Kv8Params
           uint32_t s[QP * RW];
           tmem_ld<QP * RW>(t_s + b * NQ, s);
 #pragma unroll
-          for (int i = 0; i < RP; ++i) y[i] = f2_mul(join<QP, RW>(s + 2 * i), f2_mul(factor[i], f2_both(sk)));
+          for (int i = 0; i < RP; ++i)  // (factor sk by itself may pass float32 where the scores do not)
+            y[i] = f2_mul(f2_mul(join<QP, RW>(s + 2 * i), factor[i]), f2_both(sk));
         }
         if (first_limit - t * TK < TK - 1) {  // some row does not see all of the tile
 #pragma unroll

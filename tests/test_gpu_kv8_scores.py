@@ -1,0 +1,102 @@
+"""Attention over the 8-bit cache with scores far from zero.
+
+Where all tokens that count have the same score, or one is far above the others, the
+weights do not depend on how large the scores are, and neither may the error of O:
+
+  weights exp2 2^-22 relative, its argument's roundings (numbers below 512: 2^-16
+          relative), four parts of 4 bits 2^-16 relative or 2^-29 of the row's largest
+          weight times V's scale, times codes up to 448
+  output  float32 sums, cut at 2^-23 once for each 32 tokens, merged (2^-20), one
+          rounding to bfloat16: 2^-8 (half a step is 2^-9)
+so |dO| <= (2^-14 + n 2^-28) A + 2^-29 448 n B + 2^-8 |O|, A = mean |V| of the n tokens that
+count, B = the largest scale of V over n.  A token that counts alone is V itself: V is a
+bfloat16 number, and 2^-14 is below half of a bfloat16 step.
+
+LSE is a float32 number: the score's factors, the sum and the change of base are half a
+dozen roundings of 2^-24, so |dLSE| <= 2^-21 |LSE| + 2^-20."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from exact_attention_attn_gb300 import attn_fwd_kv8, attn_fwd_status, attn_kv8_append, attn_kv8_cache, attn_kv8_read
+from exact_attention_attn_gb300.workloads import to_f64
+
+pytestmark = pytest.mark.gpu
+
+# head dim, query heads of a kv head: every number of rows of a tile
+SHAPES = [(64, 4), (128, 3), (192, 4), (256, 4), (64, 7), (128, 8), (192, 8), (256, 5), (64, 16), (128, 12), (192, 16), (256, 28), (64, 28), (128, 32)]
+P = 16
+
+
+def _dev(a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+
+
+def _cache(k, v):
+    """A cache of the tokens, and what it holds for them: V as float64 [n, H, D] and the scale of V of each token [n, H]."""
+    n, H, D = k.shape
+    cache = attn_kv8_cache(-(-n // P), H, D, P)
+    slots = _dev(np.arange(n))
+    attn_kv8_append(k, v, slots, cache, P)
+    _, held = attn_kv8_read(slots, cache, P)
+    tail = cache[..., P * D:].reshape(-1, H, 16 * D + 16)[..., 16 * D + 4:16 * D + 8].contiguous().view(torch.float32)
+    return cache, to_f64(held).transpose(1, 0, 2), np.repeat(to_f64(tail)[..., 0], 16, 0)[:n]
+
+
+def _attend(q, cache, lens, long_table, scale, causal=True):
+    """One query token a request, each request the first lens[r] tokens of the cache."""
+    B = len(lens)
+    pages = cache.shape[0]
+    table = np.full((B, 80000 // P if long_table else pages), -1)
+    table[:, :pages] = np.arange(pages)
+    o, l = attn_fwd_kv8(q, _dev(np.arange(B + 1)), _dev(lens), _dev(table), cache, P, scale=scale, causal=causal)
+    assert attn_fwd_status() == 0
+    return to_f64(o), to_f64(l)
+
+
+def _check_mean(o, v, unit):
+    """o [heads, D]: the mean of v [n, D]."""
+    n = len(v)
+    O, A = v.mean(0), np.abs(v).mean(0)
+    tol = (2.0 ** -14 + n * 2.0 ** -28) * A + 2.0 ** -29 * 448 * unit.max() + 2.0 ** -8 * np.abs(O)
+    err = np.abs(o - O)
+    assert (err <= tol).all(), (err / tol).max()
+
+
+def _values(n, D, seed, exps):
+    """bfloat16 [n, 1, D], blocks of 16 tokens of sizes 2^exps in turn."""
+    x = torch.randn((n, 1, D), generator=torch.Generator().manual_seed(seed), dtype=torch.float64)
+    size = 2.0 ** torch.tensor([float(exps[i // 16 % len(exps)]) for i in range(n)], dtype=torch.float64)
+    return (x.clamp(-3, 3) * size[:, None, None]).to(torch.bfloat16).cuda()
+
+
+def _one_dim(n, D, value):
+    x = torch.zeros((n, 1, D), dtype=torch.bfloat16, device="cuda")
+    x[..., D - 5] = value
+    return x
+
+
+@pytest.mark.parametrize("D,group", SHAPES)
+@pytest.mark.parametrize("long_table", [False, True])
+def test_large_q_and_large_k_whose_scores_are_small(D, group, long_table):
+    # their largest values' product passes 2^128: in dims where the other one is zero, cancelling, or of other tokens of the block
+    n, half = 200, D // 2
+    v = _values(n, D, 1, [0, 2])
+    q = torch.zeros((3, group, D), dtype=torch.bfloat16, device="cuda")
+    q[0, :, :half] = 2.0 ** 80
+    q[1, :, 3], q[1, :, 9] = 2.0 ** 90, 2.0 ** 90
+    q[2, :, 0] = -1.5 * 2.0 ** 99
+    k = torch.zeros((n, 1, D), dtype=torch.bfloat16, device="cuda")
+    k[:, :, half:] = 1.75 * 2.0 ** 80
+    k[::3, :, half:] *= -1
+    k[:, :, 3], k[:, :, 9] = 2.0 ** 70, -(2.0 ** 70)
+    for rows in (slice(0, n), slice(5, n, 16)):  # (or all but one token in each block are zero)
+        x = torch.zeros_like(k)
+        x[rows] = k[rows]
+        cache, held, unit = _cache(x, v)
+        o, l = _attend(q, cache, [n, n, n], long_table, 0.5)
+        for r in range(3):
+            assert (np.abs(l[r] - math.log(n)) <= 2.0 ** -20 * (1 + math.log(n))).all(), (r, l[r])
+            _check_mean(o[r], held[:, 0], unit[:, 0])
