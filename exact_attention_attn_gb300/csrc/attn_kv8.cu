@@ -17,14 +17,18 @@
 // of 128 rows and 32 of the sum takes 50 clocks with up to 64 columns, 56 with 96, 64
 // with 128.
 //
-// Scales.  A token's score takes the block's scale of K as a factor, y = s sk c. The
-// block's scale of V is joined to its weight in the exponent: P = 2^(z - M) with z = y
-// + log2 sv and M a reference per row, 4 below the largest z when it was set and set
-// again only when some z exceeds it by 8 (then the accumulators are multiplied).  So a
-// token's product with V counts by its size, whatever other tokens' scales are.  The
-// sum l of the weights has a reference of its own.  Exponents, references, l and
-// accumulators are float32; what is rounded to fewer bits are the parts of Q and P
-// above and O, once, to bfloat16.
+// Scales.  A token's score takes the block's scale of K as a factor, y = s c sk.  A row
+// has two references, Y of its scores and E of V's scales: l = sum 2^(y - Y), and the
+// block's scale of V is joined to the weight in the exponent, P = 2^((y - Y) + (log2 sv
+// - E)), so that O = 2^E / l times the accumulators and a token's product with V counts
+// by its size, whatever other tokens' scales are.  The first difference is exact where
+// it matters and the second is one of small numbers, so scores of any size leave V's
+// scale its place.  (With one reference of y + log2 sv, scores past 2^24 rounded the scale
+// away: O was off by its power of two.)  Y is the largest score when it was set, and set
+// again when one exceeds it by 60; E lets the largest exponent be 4 when it is set, and is set
+// again when one exceeds 8 (then the accumulators are multiplied).  Exponents,
+// references, l and accumulators are float32; what is rounded to fewer bits are the
+// parts of Q and P above and O, once, to bfloat16.
 //
 // Hidden tokens have weight 0 in P; V's codes of tokens past the length are zeroed in
 // shared memory first, so that nothing which a page holds there (0 times NaN) reaches a
@@ -98,10 +102,11 @@ constexpr int kMaxRows = 32;
 constexpr int kMaxRequests = ATTN_KV8_MAX_REQUESTS;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNoRef = -1e37f;  // reference of a row that has seen no token
-constexpr float kBelow = 4.f;     // a new reference lies this much below the largest z ...
-constexpr float kAbove = 8.f;     // ... and holds until z exceeds it by this much: weights stay below e4m3's 448
-constexpr float kSumAbove = 60.f; // the same for the references of l
+constexpr float kNoRef = -1e37f;  // references Y and
+constexpr float kNoExp = -1e30f;  // E of a row that has seen no token
+constexpr float kBelow = 4.f;     // a new E lets the largest exponent of P be this much ...
+constexpr float kAbove = 8.f;     // ... and holds until one exceeds this: weights stay below e4m3's 448
+constexpr float kSumAbove = 60.f; // the same for Y, which is the largest score when it is set
 constexpr float kStep = 32.f;     // 2^5, between the parts of Q and P
 constexpr int kSmemMax = 232448;
 // What a CTA waits at its end for its own copies and products, whatever the limit of the other waits is.
@@ -119,7 +124,7 @@ struct Kv8Params {
   int cluster;       // CTAs that share an item, one item each; 0: pieces of the line
   float scale_log2;  // scale * log2 e
   float *ws_o;       // partial O of cut items: [CTAs][2][R][D]
-  float4 *ws_ml;     // their references of O and l, and l: [CTAs][2][R]
+  float4 *ws_ml;     // their references E and Y, and l: [CTAs][2][R]
   int4 *ws_cut;      // [CTAs][2]: the item that each CTA leaves unfinished
   int *status;
   uint64_t wait_limit_ns;
@@ -228,11 +233,14 @@ struct Shared {
   float row_factor[2][kMaxRows];
   int row_limit[2][kMaxRows];
   int64_t row_out[2][kMaxRows];
-  float2 warp_max[2][4][kMaxRows];  // [turn][warp of the group][row]: largest z and y
-  float warp_sum[4][kMaxRows];      // [warp of the group][row]
+  // [row][warp of the group]: the largest y, and the largest (y - that) + log2 sv
+  __align__(16) float warp_y[kMaxRows][4], warp_z[kMaxRows][4];
+  // [softmax warp][row of the group]: references E and Y, negated, what their last change takes the accumulators by, and
+  // l by (at an item's end the warp's sum of l)
+  __align__(16) float ref_e[8][kMaxRows / 2], ref_y[8][kMaxRows / 2], by_o[8][kMaxRows / 2], warp_l[8][kMaxRows / 2];
   float row_weight[kMaxRows];       // [group][row], or [row]: what turns accumulators into the output
-  float4 group_ml[2][4];            // [group][row]: the references of O and l of groups that have the tiles in turn
-  float4 part_ml[kMaxRows];                // a cluster's CTA: the references of O and l, and l, of its part's rows
+  float4 group_ml[2][4];            // [group][row]: the references E and Y of groups that have the tiles in turn
+  float4 part_ml[kMaxRows];                // a cluster's CTA: the references E and Y, and l, of its part's rows
 };
 
 __device__ __forceinline__ void raise_abort(Shared *sh, int *status) {
@@ -255,11 +263,11 @@ __device__ __forceinline__ bool any_softmax(int group, bool yes) {
   return r != 0;
 }
 
-// The largest of the warp's values; NaN counts as none.
+// The largest of the warp's values; NaN counts as none (all NaN: NaN).
 __device__ __forceinline__ float warp_largest(float x) {
-  const int b = __float_as_int(x == x ? x : -INFINITY);
-  const int m = __reduce_max_sync(0xffffffffu, b < 0 ? b ^ 0x7fffffff : b);  // floats in the order of integers
-  return __int_as_float(m < 0 ? m ^ 0x7fffffff : m);
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
 }
 
 // Two e4m3 codes as a pair of floats.
@@ -327,6 +335,15 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
   tmem_wait_ld();
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i])::"memory");  // no use of them may move before the wait
+}
+
+// References (E, Y) of a part of a row's tokens, as E beside another Y: what counts of
+// it there.  Parts of a row are joined by their largest Y and, beside that, their largest E.
+__device__ __forceinline__ float beside(float e, float y, float all_y) { return (y - all_y) + e; }
+// What brings the part's accumulators to references (all_e, all_y).  (The scores' difference comes first: it is exact
+// where it matters.)
+__device__ __forceinline__ float part_factor(float e, float y, float all_e, float all_y) {
+  return ex2_approx((y - all_y) + (e - all_e));
 }
 
 // Row q of a request's rows (query token x head of the group) in the output.
@@ -858,7 +875,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv8_kernel(const Kv8Params
   } else {
     // ---------------- softmax, and the items' ends
     const int group = warp >> 2, key = tid & 127, wq = warp & 3;  // key: the token of the tile, and the dim of the output
-    int stage = 0, sphase = 0, slot = 0, iphase = 0, qb = 0, qphase = 0, turn = 0;
+    int stage = 0, sphase = 0, slot = 0, iphase = 0, qb = 0, qphase = 0;
     uint32_t n_tile = 0;
     bool fail = false;
     const uint32_t t_lanes = (uint32_t)(wq * 32) << 16;
@@ -875,12 +892,17 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv8_kernel(const Kv8Params
       if (any_at_end(fail || !it.more)) break;
       if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
       if (++slot == kItems) slot = 0, iphase ^= 1;
-      // pairs of rows: references of O and l (negated), l, and what turns sums into scores
+      // pairs of rows: references E and Y (negated), l, and what turns sums into scores
       constexpr int RP = RW / 2;
-      uint64_t ref[RP], sref[RP], l[RP], factor[RP];
+      uint64_t eref[RP], yref[RP], l[RP], factor[RP];
+      if (lane < RW) {
+        sh->ref_e[warp][lane] = -kNoExp;
+        sh->ref_y[warp][lane] = -kNoRef;
+      }
 #pragma unroll
       for (int i = 0; i < RP; ++i) {
-        ref[i] = sref[i] = f2_both(-kNoRef);
+        eref[i] = f2_both(-kNoExp);
+        yref[i] = f2_both(-kNoRef);
         l[i] = f2_both(0.f);
         factor[i] = f2_pack(sh->row_factor[qb][row0 + 2 * i], sh->row_factor[qb][row0 + 2 * i + 1]);
       }
@@ -917,13 +939,13 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv8_kernel(const Kv8Params
             y[i] = f2_pack(key > limits[2 * i] - t * TK ? -INFINITY : f2_low(y[i]),
                            key > limits[2 * i + 1] - t * TK ? -INFINITY : f2_high(y[i]));
         }
-        // z - ref and y - sref: exponents of the weights
+        // y - Y and (y - Y) + (lv - E): exponents of the weights in l and in P
         uint64_t tz[RP], ty[RP];
         auto exponents = [&]() {
 #pragma unroll
           for (int i = 0; i < RP; ++i) {
-            tz[i] = f2_add(f2_add(y[i], f2_both(lv)), ref[i]);
-            ty[i] = f2_add(y[i], sref[i]);
+            ty[i] = f2_add(y[i], yref[i]);
+            tz[i] = f2_add(ty[i], f2_add(f2_both(lv), eref[i]));
           }
         };
         exponents();
@@ -934,37 +956,44 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv8_kernel(const Kv8Params
           most_y = max3f(most_y, f2_low(ty[i]), f2_high(ty[i]));
         }
         if (any_softmax(group, fail || most_z > kAbove || most_y > kSumAbove)) {
-          // new references, from the tile's largest z and y
-          float2(*const top)[kMaxRows] = sh->warp_max[turn];
-          turn ^= 1;
+          // New references, from the tile's scores: a row a lane, each warp for itself (unrolled over the rows it is long
+          // code that is run a few times an item: 16 requests of 4 query tokens, D 256, 500 tokens 10.8 -> 11.5 us)
 #pragma unroll
-          for (int r = 0; r < RW; ++r) {
-            const float x = r & 1 ? f2_high(y[r / 2]) : f2_low(y[r / 2]);
-            const float z = warp_largest(x + lv), w = warp_largest(x);
-            if (lane == 0) top[wq][group * RW + r] = make_float2(z, w);
+          for (int i = 0; i < RP; ++i) {
+            const float w0 = warp_largest(f2_low(y[i])), w1 = warp_largest(f2_high(y[i]));
+            const uint64_t z = f2_add(f2_add(y[i], f2_pack(-w0, -w1)), f2_both(lv));
+            const float z0 = warp_largest(f2_low(z)), z1 = warp_largest(f2_high(z));
+            if (lane == 0) {
+              sh->warp_y[group * RW + 2 * i][wq] = w0;
+              sh->warp_y[group * RW + 2 * i + 1][wq] = w1;
+              sh->warp_z[group * RW + 2 * i][wq] = z0;
+              sh->warp_z[group * RW + 2 * i + 1][wq] = z1;
+            }
           }
           if (any_softmax(group, fail)) {
             fail = true;
             break;
           }
-          float f[RW];
+          if (lane < RW) {  // (fmaxf leaves out the NaN of a warp that has no score)
+            const float4 w = *reinterpret_cast<const float4 *>(sh->warp_y[group * RW + lane]);
+            const float4 z = *reinterpret_cast<const float4 *>(sh->warp_z[group * RW + lane]);
+            const float e = -sh->ref_e[warp][lane], s = -sh->ref_y[warp][lane];
+            const float y_now = fmaxf(s, fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)));
+            const float z_now = fmaxf(fmaxf(beside(z.x, w.x, y_now), beside(z.y, w.y, y_now)),
+                                      fmaxf(beside(z.z, w.z, y_now), beside(z.w, w.w, y_now)));
+            const float e_now = fmaxf(beside(e, s, y_now), z_now - kBelow);
+            sh->ref_e[warp][lane] = -e_now;
+            sh->ref_y[warp][lane] = -y_now;
+            sh->by_o[warp][lane] = part_factor(e, s, e_now, y_now);
+            sh->warp_l[warp][lane] = ex2_approx(s - y_now);
+          }
+          __syncwarp();
+          auto rows2 = [&](const float(&x)[8][kMaxRows / 2], int i) { return *reinterpret_cast<const uint64_t *>(&x[warp][2 * i]); };
 #pragma unroll
           for (int i = 0; i < RP; ++i) {
-            float now[2], snow[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int all = group * RW + 2 * i + k;
-              const float2 a = top[0][all], c = top[1][all], d = top[2][all], e = top[3][all];
-              const float was = -(k ? f2_high(ref[i]) : f2_low(ref[i])), swas = -(k ? f2_high(sref[i]) : f2_low(sref[i]));
-              now[k] = fmaxf(was, fmaxf(fmaxf(a.x, c.x), fmaxf(d.x, e.x)) - kBelow);
-              snow[k] = fmaxf(swas, fmaxf(fmaxf(a.y, c.y), fmaxf(d.y, e.y)));
-              f[2 * i + k] = ex2_approx(was - now[k]);
-              now[k] = -now[k];
-              snow[k] = -snow[k];
-            }
-            l[i] = f2_mul(l[i], f2_pack(ex2_approx(snow[0] - f2_low(sref[i])), ex2_approx(snow[1] - f2_high(sref[i]))));
-            ref[i] = f2_pack(now[0], now[1]);
-            sref[i] = f2_pack(snow[0], snow[1]);
+            eref[i] = rows2(sh->ref_e, i);
+            yref[i] = rows2(sh->ref_y, i);
+            l[i] = f2_mul(l[i], rows2(sh->warp_l, i));
           }
           exponents();
           if (some) {
@@ -978,7 +1007,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv8_kernel(const Kv8Params
                 uint32_t o[16];
                 tmem_ld<16>(t_acc + hf * NP + c0, o);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f[(c0 + c) % RW]);
+                for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * sh->by_o[warp][(c0 + c) % RW]);
                 tmem_st16(t_acc + hf * NP + c0, o);
               }
             tmem_wait_st();
@@ -1032,17 +1061,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv8_kernel(const Kv8Params
       }
 #pragma unroll
       for (int o = 16 / RW; o >= 1; o >>= 1) ls[0] += __shfl_xor_sync(0xffffffffu, ls[0], o);
-      if (lane % (32 / RW) == 0) sh->warp_sum[wq][group * RW + row] = ls[0];
-      if (TURNS && key < RW) {
-        float a = 0.f, c = 0.f;
-#pragma unroll
-        for (int r = 0; r < RW; ++r)
-          if (key == r) {
-            a = -(r & 1 ? f2_high(ref[r / 2]) : f2_low(ref[r / 2]));
-            c = -(r & 1 ? f2_high(sref[r / 2]) : f2_low(sref[r / 2]));
-          }
-        sh->group_ml[group][key] = make_float4(a, c, some ? 1.f : 0.f, 0.f);
-      }
+      if (lane % (32 / RW) == 0) sh->warp_l[warp][row] = ls[0];
+      if (TURNS && key < RW)
+        sh->group_ml[group][key] = make_float4(-sh->ref_e[warp][lane], -sh->ref_y[warp][lane], some ? 1.f : 0.f, 0.f);
       if (some && !fail) {
         // (one barrier for each of two tiles in turn: when the last tile's scores were there, the product of the tile
         // three before it was done, that of the one before it perhaps not, so a single barrier could be two phases
@@ -1055,18 +1076,19 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv8_kernel(const Kv8Params
         fail = true;
         break;
       }
-      auto sum_of = [&](int i) {
-        return (sh->warp_sum[0][i] + sh->warp_sum[1][i]) + (sh->warp_sum[2][i] + sh->warp_sum[3][i]);
+      auto sum_of = [&](int g, int row) {
+        const float(*const x)[kMaxRows / 2] = sh->warp_l + 4 * g;
+        return (x[0][row] + x[1][row]) + (x[2][row] + x[3][row]);
       };
       if (TURNS && tid < RW) {
         // both groups' parts of a row, brought to the larger references
         const float4 u = sh->group_ml[0][tid], w = sh->group_ml[1][tid];
-        const float a = fmaxf(u.x, w.x), c = fmaxf(u.y, w.y);
-        const float x = sum_of(tid) * ex2_approx(u.y - c) + sum_of(RW + tid) * ex2_approx(w.y - c);
+        const float c = fmaxf(u.y, w.y), a = fmaxf(beside(u.x, u.y, c), beside(w.x, w.y, c));
+        const float x = sum_of(0, tid) * ex2_approx(u.y - c) + sum_of(1, tid) * ex2_approx(w.y - c);
         const bool none = x == 0.f;
-        const float lg = log2f(x), f = it.slot >= 0 ? 1.f : none ? 0.f : ex2_approx(a - c - lg);
-        sh->row_weight[tid] = ex2_approx(u.x - a) * f;
-        sh->row_weight[RW + tid] = ex2_approx(w.x - a) * f;
+        const float lg = log2f(x), f = it.slot >= 0 ? 1.f : none ? 0.f : ex2_approx(a - lg);
+        sh->row_weight[tid] = part_factor(u.x, u.y, a, c) * f;
+        sh->row_weight[RW + tid] = part_factor(w.x, w.y, a, c) * f;
         if (tid < it.rows) {
           if (it.slot < 0)
             p.lse[sh->row_out[qb][tid]] = none ? -INFINITY : (c + lg) * kLn2;
@@ -1078,17 +1100,10 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv8_kernel(const Kv8Params
       }
       if (!TURNS && key < RW) {
         const int all = row0 + key;
-        const float x = sum_of(all);
-        float a = 0.f, c = 0.f;
-#pragma unroll
-        for (int r = 0; r < RW; ++r)
-          if (key == r) {
-            a = -(r & 1 ? f2_high(ref[r / 2]) : f2_low(ref[r / 2]));
-            c = -(r & 1 ? f2_high(sref[r / 2]) : f2_low(sref[r / 2]));
-          }
+        const float x = sum_of(group, key), a = -sh->ref_e[warp][lane], c = -sh->ref_y[warp][lane];
         const bool none = x == 0.f;
         const float lg = log2f(x);
-        sh->row_weight[all] = it.slot >= 0 ? 1.f : none ? 0.f : ex2_approx(a - c - lg);
+        sh->row_weight[all] = it.slot >= 0 ? 1.f : none ? 0.f : ex2_approx(a - lg);
         if (all < it.rows) {
           if (it.slot < 0)
             p.lse[sh->row_out[qb][all]] = none ? -INFINITY : (c + lg) * kLn2;
@@ -1180,21 +1195,22 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv8_kernel(const Kv8Params
       for (int i = rank * S::THREADS + tid; i < it.rows * (D / 4); i += p.cluster * S::THREADS) {
         const int row = i / (D / 4), dim = (i % (D / 4)) * 4;
         float4 ml[kMostCluster], v[kMostCluster];
-        float ref = kNoRef, m = kNoRef, l = 0.f;
+        float e = kNoExp, m = kNoRef, l = 0.f;
 #pragma unroll
         for (int c = 0; c < kMostCluster; ++c) {
-          ml[c] = make_float4(kNoRef, kNoRef, 0.f, 0.f);
+          ml[c] = make_float4(kNoExp, kNoRef, 0.f, 0.f);
           v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (c >= p.cluster) continue;
           ml[c] = ld_cluster_f4(mapa_shared(ml_s + row * 16, c));
           v[c] = ld_cluster_f4(mapa_shared(o_s + (row * D + dim) * 4, c));
-          ref = fmaxf(ref, ml[c].x);
           m = fmaxf(m, ml[c].y);
         }
+#pragma unroll
+        for (int c = 0; c < kMostCluster; ++c) e = fmaxf(e, beside(ml[c].x, ml[c].y, m));
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int c = 0; c < kMostCluster; ++c) {
-          const float f = ex2_approx(ml[c].x - ref);
+          const float f = part_factor(ml[c].x, ml[c].y, e, m);
           l = fmaf(ml[c].z, ex2_approx(ml[c].y - m), l);
           o.x = fmaf(f, v[c].x, o.x);
           o.y = fmaf(f, v[c].y, o.y);
@@ -1202,7 +1218,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv8_kernel(const Kv8Params
           o.w = fmaf(f, v[c].w, o.w);
         }
         const bool none = l == 0.f;
-        const float lg = log2f(l), w = none ? 0.f : ex2_approx(ref - m - lg);
+        const float lg = log2f(l), w = none ? 0.f : ex2_approx(e - lg);
         const int64_t at = out_row(p, it.t0, it.h, it.row0 + row);
         *reinterpret_cast<uint2 *>(p.o + at * D + dim) =
             make_uint2(pack_bf16x2(o.x * w, o.y * w), pack_bf16x2(o.z * w, o.w * w));
@@ -1214,8 +1230,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kv8_kernel(const Kv8Params
 }
 
 // Merges the item that CTA blockIdx.x of the first kernel began and left unfinished:
-// row blockIdx.y, its parts in the order of the tokens.  With M = max ref_i and
-// m = max m_i:  l = sum 2^(m_i - m) l_i,  O = 2^(M - m) sum 2^(ref_i - M) O_i / l.
+// row blockIdx.y, its parts in the order of the tokens.  With Y = max Y_i and
+// E = max (Y_i - Y) + E_i:  l = sum 2^(Y_i - Y) l_i,  O = 2^E sum 2^((Y_i - Y) + (E_i - E)) O_i / l.
 // Two dependent passes through L2, launched ahead of the first kernel's end: about 4 us.
 constexpr int kMergeWarps = 8;
 
@@ -1232,7 +1248,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attn_kv8_merge_kernel(const 
   if (row >= d.w) return;
   auto at = [&](int i) { return ((int64_t)(cta + i) * 2 + (i == 0 ? 1 : 0)) * R + row; };
   // a warp sums every eighth part, several in flight, with references of its own
-  float ref = kNoRef, m = kNoRef, l = 0.f;
+  float e = kNoExp, m = kNoRef, l = 0.f;
   float4 o[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1241,7 +1257,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attn_kv8_merge_kernel(const 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kMergeWarps;
-      ml[u] = make_float4(kNoRef, kNoRef, 0.f, 0.f);
+      ml[u] = make_float4(kNoExp, kNoRef, 0.f, 0.f);
 #pragma unroll
       for (int v = 0; v < V; ++v) x[u][v] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i >= n) continue;
@@ -1250,18 +1266,21 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attn_kv8_merge_kernel(const 
       for (int v = 0; v < V; ++v)
         if (v * 128 + lane * 4 < D) x[u][v] = *reinterpret_cast<const float4 *>(p.ws_o + at(i) * D + v * 128 + lane * 4);
     }
-    float now = ref, mnow = m;
+    float mnow = m;
 #pragma unroll
-    for (int u = 0; u < U; ++u) now = fmaxf(now, ml[u].x), mnow = fmaxf(mnow, ml[u].y);
-    const float f0 = ex2_approx(ref - now);
+    for (int u = 0; u < U; ++u) mnow = fmaxf(mnow, ml[u].y);
+    float enow = beside(e, m, mnow);
+#pragma unroll
+    for (int u = 0; u < U; ++u) enow = fmaxf(enow, beside(ml[u].x, ml[u].y, mnow));
+    const float f0 = part_factor(e, m, enow, mnow);
     l *= ex2_approx(m - mnow);
-    ref = now;
+    e = enow;
     m = mnow;
 #pragma unroll
     for (int v = 0; v < V; ++v) o[v] = make_float4(o[v].x * f0, o[v].y * f0, o[v].z * f0, o[v].w * f0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const float f = ex2_approx(ml[u].x - ref);
+      const float f = part_factor(ml[u].x, ml[u].y, e, m);
       l = fmaf(ml[u].z, ex2_approx(ml[u].y - m), l);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -1275,20 +1294,23 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attn_kv8_merge_kernel(const 
 #pragma unroll
   for (int v = 0; v < V; ++v)
     if (v * 128 + lane * 4 < D) *reinterpret_cast<float4 *>(&part[warp][v * 128 + lane * 4]) = o[v];
-  if (lane == 0) part_ml[warp] = make_float4(ref, m, l, 0.f);
+  if (lane == 0) part_ml[warp] = make_float4(e, m, l, 0.f);
   __syncthreads();
   l = 0.f;
+  e = kNoExp;
 #pragma unroll
-  for (int i = 0; i < kMergeWarps; ++i) ref = fmaxf(ref, part_ml[i].x), m = fmaxf(m, part_ml[i].y);
+  for (int i = 0; i < kMergeWarps; ++i) m = fmaxf(m, part_ml[i].y);
+#pragma unroll
+  for (int i = 0; i < kMergeWarps; ++i) e = fmaxf(e, beside(part_ml[i].x, part_ml[i].y, m));
 #pragma unroll
   for (int i = 0; i < kMergeWarps; ++i) l = fmaf(part_ml[i].z, ex2_approx(part_ml[i].y - m), l);
   const bool none = l == 0.f;
-  const float lg = log2f(l), w = none ? 0.f : ex2_approx(ref - m - lg);
+  const float lg = log2f(l), w = none ? 0.f : ex2_approx(e - lg);
   const int64_t to = out_row(p, d.x, d.y, d.z + row);
   for (int dim = threadIdx.x; dim < D; dim += kMergeWarps * 32) {
     float x = 0.f;
 #pragma unroll
-    for (int i = 0; i < kMergeWarps; ++i) x = fmaf(part[i][dim], ex2_approx(part_ml[i].x - ref), x);
+    for (int i = 0; i < kMergeWarps; ++i) x = fmaf(part[i][dim], part_factor(part_ml[i].x, part_ml[i].y, e, m), x);
     p.o[to * D + dim] = __float2bfloat16_rn(x * w);
   }
   if (threadIdx.x == 0) p.lse[to] = none ? -INFINITY : (m + lg) * kLn2;

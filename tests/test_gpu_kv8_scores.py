@@ -78,6 +78,70 @@ def _one_dim(n, D, value):
     return x
 
 
+def _scores(power, sign):
+    """q and K whose product is about sign 2^power, both bfloat16 numbers (K an e4m3 number times a power of two)."""
+    a = power // 2
+    return 1.3125 * 2.0 ** a * sign, 1.25 * 2.0 ** (power - a), 1.3125 * 1.25 * 2.0 ** power * sign
+
+
+POWERS = [10, 20, 24, 25, 27, 30, 41, 60, 100]
+
+
+@pytest.mark.parametrize("D,group", SHAPES)
+@pytest.mark.parametrize("long_table", [False, True])
+def test_one_token_is_its_value(D, group, long_table):
+    for exp in (-90, -7, 0, 1, 30, 117):
+        v = _values(1, D, D + exp, [exp])
+        for power in POWERS:
+            for sign in (1, -1):
+                a, b, s = _scores(power, sign)
+                cache, held, _ = _cache(_one_dim(1, D, b), v)
+                q = _one_dim(1, D, a).expand(1, group, D).contiguous()
+                o, l = _attend(q, cache, [1], long_table, 1.0)
+                assert (np.abs(l - s) <= 2.0 ** -21 * abs(s) + 2.0 ** -20).all(), (exp, power, sign, l[0, 0], s)
+                assert np.array_equal(o[0], np.broadcast_to(held[0], o[0].shape)), (exp, power, sign)
+
+
+@pytest.mark.parametrize("D,group", SHAPES)
+@pytest.mark.parametrize("long_table", [False, True])
+@pytest.mark.parametrize("exps", [[-7, -8], [0, -6, 3, -100], [5, 100, 40]])
+def test_equal_tokens_have_equal_weights(D, group, long_table, exps):
+    # of one block, of blocks of one tile with other scales, of several tiles, of cut items and of clusters
+    lens = [2, 17, 40, 200, 700, 1500]
+    n = max(lens)
+    v = _values(n, D, D, exps)
+    for power in POWERS:
+        for sign in (1, -1):
+            a, b, s = _scores(power, sign)
+            cache, held, unit = _cache(_one_dim(n, D, b), v)
+            q = _one_dim(len(lens), D, a).expand(len(lens), group, D).contiguous()
+            o, l = _attend(q, cache, lens, long_table, 1.0)
+            for r, m in enumerate(lens):
+                L = s + math.log(m)
+                assert (np.abs(l[r] - L) <= 2.0 ** -21 * abs(L) + 2.0 ** -20).all(), (power, sign, m)
+                _check_mean(o[r], held[:m, 0], unit[:m, 0])
+
+
+@pytest.mark.parametrize("D,group", SHAPES)
+@pytest.mark.parametrize("long_table", [False, True])
+def test_a_heavy_token_among_others(D, group, long_table):
+    # its score is far above the others', whose V are far larger or far smaller
+    n = 600
+    for where in (0, 130, 599):
+        for exps in ([-30, 40], [50, -5]):
+            v = _values(n, D, where, exps)
+            for power in POWERS[1:]:
+                for sign in (1, -1):
+                    a, b, s = _scores(power, sign)
+                    k = _one_dim(n, D, b if sign < 0 else -b)  # the others' scores are -|s|
+                    k[where] *= -1
+                    cache, held, _ = _cache(k, v)
+                    q = _one_dim(1, D, a).expand(1, group, D).contiguous()
+                    o, l = _attend(q, cache, [n], long_table, 1.0)
+                    assert (np.abs(l - abs(s)) <= 2.0 ** -21 * abs(s)).all(), (where, power, sign)
+                    assert np.array_equal(o[0], np.broadcast_to(held[where], o[0].shape)), (where, power, sign, exps)
+
+
 @pytest.mark.parametrize("D,group", SHAPES)
 @pytest.mark.parametrize("long_table", [False, True])
 def test_large_q_and_large_k_whose_scores_are_small(D, group, long_table):
