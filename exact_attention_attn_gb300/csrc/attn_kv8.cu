@@ -75,6 +75,7 @@
 // each). 64 of 2730 with 16 rows 80, with 28 122 (53): the softmax's arithmetic, every
 // weight split in four.  One request of 129 tokens 6.3.
 #include <cuda_bf16.h>
+#include <float.h>
 #include <math.h>
 #include <string.h>
 
@@ -102,8 +103,8 @@ constexpr int kMaxRows = 32;
 constexpr int kMaxRequests = ATTN_KV8_MAX_REQUESTS;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNoRef = -1e37f;  // references Y and
-constexpr float kNoExp = -1e30f;  // E of a row that has seen no token
+// References of a row that has seen no token: Y is no larger than any score, and E so low that any score sets both.
+constexpr float kNoRef = -FLT_MAX, kNoExp = -1e30f;
 constexpr float kBelow = 4.f;     // a new E lets the largest exponent of P be this much ...
 constexpr float kAbove = 8.f;     // ... and holds until one exceeds this: weights stay below e4m3's 448
 constexpr float kSumAbove = 60.f; // the same for Y, which is the largest score when it is set

@@ -637,8 +637,9 @@ ATTN_API int attn_kv8_read(const void *cache, int num_pages, const int *slots, v
  * largest value on (else to 2^-27 of that), a weight times V's scale to 2^-16 relative or
  * 2^-28 of the largest such product of the row, whichever is coarser.  O is rounded
  * once to bf16.
- *        Ranges: |q| scale and K up to 2^100 each, their scores finite in float32;
- *        V any finite bf16.  A marked token makes NaN what sees it: K's mark O and
+ *        Ranges: |q| scale and K up to 2^100 each, their scores below 2^127 in
+ *        magnitude; V any finite bf16.  Scores of any size leave O's error as it is
+ *        where the tokens' scores are equal or far apart.  A marked token makes NaN what sees it: K's mark O and
  *        LSE, V's O.  Scales must be powers of two, from 2^-100 to 2^120, as
  *        attn_kv8_append makes them.
  * D      64, 128, 192 or 256.  max_pages * page_size < 2^31 - 1024.

@@ -84,7 +84,7 @@ def _scores(power, sign):
     return 1.3125 * 2.0 ** a * sign, 1.25 * 2.0 ** (power - a), 1.3125 * 1.25 * 2.0 ** power * sign
 
 
-POWERS = [10, 20, 24, 25, 27, 30, 41, 60, 100]
+POWERS = [10, 20, 24, 25, 27, 30, 41, 60, 100, 124]
 
 
 @pytest.mark.parametrize("D,group", SHAPES)
@@ -164,3 +164,36 @@ def test_large_q_and_large_k_whose_scores_are_small(D, group, long_table):
         for r in range(3):
             assert (np.abs(l[r] - math.log(n)) <= 2.0 ** -20 * (1 + math.log(n))).all(), (r, l[r])
             _check_mean(o[r], held[:, 0], unit[:, 0])
+
+
+@pytest.mark.parametrize("D,group", SHAPES)
+@pytest.mark.parametrize("long_table", [False, True])
+def test_scores_next_to_the_end_of_float32(D, group, long_table):
+    # up to 2^127, next to -2^127 too, where "no token yet" must not be taken for a reference
+    lens = [1, 16, 129, 700]
+    n = max(lens)
+    v = _values(n, D, 1, [-7, -5])
+    for a, b in ((2.0 ** 63, 2.0 ** 60), (2.0 ** 63, 1.25 * 2.0 ** 61), (2.0 ** 63, 1.5 * 2.0 ** 63), (2.0 ** 63, 1.875 * 2.0 ** 63)):
+        for sign in (1, -1):
+            s = sign * a * b
+            cache, held, unit = _cache(_one_dim(n, D, b), v)
+            q = _one_dim(len(lens), D, a * sign).expand(len(lens), group, D).contiguous()
+            o, l = _attend(q, cache, lens, long_table, 1.0)
+            for r, m in enumerate(lens):
+                assert (np.abs(l[r] - s) <= 2.0 ** -21 * abs(s)).all(), (s, m, l[r])
+                _check_mean(o[r], held[:m, 0], unit[:m, 0])
+
+
+@pytest.mark.parametrize("D,group", SHAPES)
+def test_rows_that_see_no_token_beside_scores_far_below_zero(D, group):
+    # three query tokens of two cached ones: the first sees none, the others' scores are -2^126
+    v = _values(2, D, 3, [0])
+    cache, held, _ = _cache(_one_dim(2, D, 2.0 ** 63), v)
+    table = _dev([[0]])
+    q = _one_dim(3, D, -(2.0 ** 63)).expand(3, group, D).contiguous()
+    o, l = attn_fwd_kv8(q, _dev([0, 3]), _dev([2]), table, cache, P, scale=1.0)
+    assert attn_fwd_status() == 0
+    o, l = to_f64(o), to_f64(l)
+    assert (o[0] == 0).all() and np.isneginf(l[0]).all()
+    assert np.array_equal(o[1], np.broadcast_to(held[0], o[1].shape)) and (np.abs(l[1:] + 2.0 ** 126) <= 2.0 ** 105).all()
+    _check_mean(o[2], held[:, 0], np.array([0.0]))
