@@ -182,7 +182,7 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
 }
 
 // The tiles of a request whose cu descends (requests could then share query tokens
-// and the line be longer than the host took it to be): the line is left empty.
+// and the line be longer than the host took it to be): no request has any work then.
 constexpr int kDescends = 1 << 30;
 
 // What a request's tiles look like, from the device arrays, with whatever they hold
@@ -437,8 +437,13 @@ __device__ __forceinline__ void find_item(const Kv8Params &p, Shared *sh, const 
   const int r0 = min(finder * per, p.B), r1 = min(r0 + per, p.B);
   const int item = (int)blockIdx.x / p.cluster, rank = (int)blockIdx.x - item * p.cluster;
   int64_t mine = r0 < r1 ? (int64_t)p.H * mine0.rt : 0;
+  bool descends = r0 < r1 && mine0.tiles >= kDescends;
 #pragma unroll 4
-  for (int r = r0 + 1; r < r1; ++r) mine += (int64_t)p.H * load_request<S>(p, r).rt;
+  for (int r = r0 + 1; r < r1; ++r) {
+    const Request q = load_request<S>(p, r);
+    mine += (int64_t)p.H * q.rt;
+    descends |= q.tiles >= kDescends;
+  }
   int64_t sum = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -448,19 +453,21 @@ __device__ __forceinline__ void find_item(const Kv8Params &p, Shared *sh, const 
   int64_t a = sum - mine;
   if (finder == 0) sh->start[0] = -1;
   if (!alone && lane == 31) sh->wsum[warp] = sum;
-  sync_finders(alone);
-  if (!alone) {
+  const bool none = alone ? __any_sync(0xffffffffu, descends) : __syncthreads_or(descends);
+  if (alone) {
+    __syncwarp();
+  } else {
 #pragma unroll
     for (int w = 0; w < S::THREADS / 32; ++w)
       if (w < warp) a += sh->wsum[w];
   }
-  if (item >= a && item < a + mine) {
+  if (!none && item >= a && item < a + mine) {
     for (int r = r0; r < r1; ++r) {
       const Request q = r == r0 ? mine0 : load_request<S>(p, r);
       const int64_t n = (int64_t)p.H * q.rt;
       if (item < a + n) {
         const int i = (int)(item - a);
-        sh->start[0] = q.tiles >= kDescends ? -1 : r;
+        sh->start[0] = r;
         sh->start[1] = i / q.rt;
         sh->start[2] = i % q.rt;
         sh->first = q;
