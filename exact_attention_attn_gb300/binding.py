@@ -80,6 +80,7 @@ def load_library() -> ctypes.CDLL:
         lib.attn_rope.restype = ci
         lib.attn_pages_assign.argtypes = [vp, ll, ci, vp, vp, ci, ci, vp, ci, vp, vp, vp, vp, vp, vp, ci, vp, vp]
         lib.attn_pages_assign.restype = ci
+        lib.attn_pages_assign_after.argtypes, lib.attn_pages_assign_after.restype = [vp, *lib.attn_pages_assign.argtypes], ci
         lib.attn_pages_release.argtypes = [vp, ll, ci, vp, vp, ci, ci, vp, ci, vp, vp, vp, vp, vp]
         lib.attn_pages_release.restype = ci
         lib.attn_kv4_page_bytes.argtypes = [ci, ci]
@@ -100,6 +101,7 @@ def load_library() -> ctypes.CDLL:
             change.restype = ci
         lib.attn_pages_own.argtypes = [vp, ll, ci, vp, vp, ci, ci, vp, ci, vp, ci, vp, vp, vp, vp, vp, vp]
         lib.attn_pages_own.restype = ci
+        lib.attn_pages_own_after.argtypes, lib.attn_pages_own_after.restype = [vp, *lib.attn_pages_own.argtypes], ci
         lib.attn_pages_compact.argtypes = [vp, ll, vp, ll, ci, vp, ci, ci, vp, vp, ci, vp, vp, ci, vp, vp, vp, ci, vp, vp, vp]
         lib.attn_pages_compact.restype = ci
         lib.attn_pages_copy.argtypes = [vp, ll, ci, ci, ll, vp, vp, ci, vp]

@@ -49,6 +49,7 @@ struct PagesParams {
   int *free_count_out;
   int B, max_tokens;
   int *cu, *slots, *positions, *info;
+  const int *after;  // info of a call that must not have been refused, or nullptr
 };
 
 // Inclusive sums of v over the warp's lanes.
@@ -103,6 +104,7 @@ __global__ void __launch_bounds__(kMaxThreads) attn_pages_kernel(const PagesPara
   const int count = *p.free_count;
   const int64_t room = (int64_t)p.max_pages << p.shift;
   int bad = (count < 0 || count > p.free_capacity) ? ATTN_PAGES_BAD_COUNT : 0;
+  if (p.after && *p.after) bad |= ATTN_PAGES_AFTER_REFUSAL;
   long long tokens = 0, pages = 0;
   for (int base = 0; base < p.B; base += threads) {
     const int r = base + threadIdx.x;
@@ -264,6 +266,15 @@ int attn_pages_assign(int *block_table, long long table_stride, int max_pages, c
                       int B, int page_size, const int *free_pages, int free_capacity, const int *free_count,
                       int *lens_out, int *free_count_out, int *cu, int *slots, int *positions, int max_tokens,
                       int *info, attn_stream_t stream) {
+  return attn_pages_assign_after(nullptr, block_table, table_stride, max_pages, lens, new_lens, B, page_size, free_pages,
+                                 free_capacity, free_count, lens_out, free_count_out, cu, slots, positions, max_tokens,
+                                 info, stream);
+}
+
+int attn_pages_assign_after(const int *after, int *block_table, long long table_stride, int max_pages, const int *lens,
+                            const int *new_lens, int B, int page_size, const int *free_pages, int free_capacity,
+                            const int *free_count, int *lens_out, int *free_count_out, int *cu, int *slots,
+                            int *positions, int max_tokens, int *info, attn_stream_t stream) {
   using namespace attn;
   const int shift = kv4_page_shift(page_size);
   if (shift < 0 || B < 0 || B > ATTN_PAGES_MAX_REQUESTS || max_pages < 0 || free_capacity < 0 || max_tokens < 0)
@@ -276,7 +287,7 @@ int attn_pages_assign(int *block_table, long long table_stride, int max_pages, c
   if (max_tokens > 0 && (!slots || !positions)) return ATTN_ERR_ARG;
   PagesParams p{};
   p.table = block_table; p.table_stride = table_stride; p.max_pages = max_pages; p.P = page_size; p.shift = shift;
-  p.lens = lens; p.lens_out = lens_out; p.arg = new_lens;
+  p.lens = lens; p.lens_out = lens_out; p.arg = new_lens; p.after = after;
   p.free_pages = const_cast<int *>(free_pages);  // only read by this kernel
   p.free_capacity = free_capacity; p.free_count = free_count; p.free_count_out = free_count_out;
   p.B = B; p.max_tokens = max_tokens;

@@ -49,6 +49,7 @@ struct SharedPagesParams {
   const int *lens;
   int *lens_out;
   const int *arg;  // parents, kept lengths or new lengths
+  const int *after;  // own: info of a call that must not have been refused, or nullptr
   int *shares, *shares_out;
   int num_pages;
   int *free_pages, *free_out;
@@ -355,6 +356,7 @@ __global__ void __launch_bounds__(kMaxThreads) attn_pages_own_kernel(const Share
     return word;
   };
   int bad = count < 0 || count > p.free_capacity ? ATTN_PAGES_BAD_COUNT : 0;
+  if (p.after && *p.after) bad |= ATTN_PAGES_AFTER_REFUSAL;
   for (int r = threadIdx.x; r < p.B; r += threads) {
     const int l = p.lens[r], n = p.arg[r];
     page[r] = kUnchanged;
@@ -727,6 +729,14 @@ int attn_pages_release_shared(int *block_table, long long table_stride, int max_
 int attn_pages_own(int *block_table, long long table_stride, int max_pages, const int *lens, const int *new_lens, int B,
                    int page_size, int *shares, int num_pages, const int *free_pages, int free_capacity,
                    const int *free_count, int *free_count_out, int *src, int *dst, int *info, attn_stream_t stream) {
+  return attn_pages_own_after(nullptr, block_table, table_stride, max_pages, lens, new_lens, B, page_size, shares, num_pages,
+                              free_pages, free_capacity, free_count, free_count_out, src, dst, info, stream);
+}
+
+int attn_pages_own_after(const int *after, int *block_table, long long table_stride, int max_pages, const int *lens,
+                         const int *new_lens, int B, int page_size, int *shares, int num_pages, const int *free_pages,
+                         int free_capacity, const int *free_count, int *free_count_out, int *src, int *dst, int *info,
+                         attn_stream_t stream) {
   using namespace attn;
   int rc = check_state(block_table, table_stride, max_pages, lens, B, page_size, shares, num_pages, free_pages, free_capacity,
                        free_count, info);
@@ -735,7 +745,7 @@ int attn_pages_own(int *block_table, long long table_stride, int max_pages, cons
   SharedPagesParams p{};
   p.table = block_table; p.table_stride = table_stride; p.max_pages = max_pages; p.P = page_size;
   p.shift = kv4_page_shift(page_size);
-  p.lens = lens; p.arg = new_lens;
+  p.lens = lens; p.arg = new_lens; p.after = after;
   p.shares = shares; p.num_pages = num_pages;
   p.free_pages = const_cast<int *>(free_pages);  // only read by this kernel
   p.free_capacity = free_capacity; p.free_count = free_count; p.free_count_out = free_count_out;

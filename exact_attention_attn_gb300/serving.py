@@ -294,8 +294,16 @@ def _page_state(table, lens, arg, arg_name, free_pages, free_count, page_size, m
     return stride, index, B, width, capacity
 
 
+def _after(info, index):
+    """The pointer of an earlier call's info, or none."""
+    if info is None:
+        return None
+    _dense(info, "after", _I32, (2,), index)
+    return info.data_ptr()
+
+
 def attn_pages_assign(table, lens, new_lens, free_pages, free_count, page_size: int, max_tokens: int, out=None,
-                      stream=None) -> dict:
+                      stream=None, after=None) -> dict:
     """Pages, slots and positions of ``new_lens`` further tokens of each request.
 
     All int32 on one device: ``table`` [B, max_pages] (updated in place),
@@ -304,7 +312,10 @@ def attn_pages_assign(table, lens, new_lens, free_pages, free_count, page_size: 
     [1], cu [B + 1], slots and positions [max_tokens], info [2] (info[0] != 0:
     the step was refused and nothing changed, see ATTN_PAGES_* in
     include/attn.h).  ``out`` may hold any of them; out["lens"] may be lens and
-    out["free_count"] free_count, for updates in place."""
+    out["free_count"] free_count, for updates in place.
+
+    ``after``: the info of the step's call before (attn_pages_own's); where that was
+    refused, so is this one (out["info"] may be the same tensor)."""
     key = plan = None
     if out and len(out) == 6:
         try:
@@ -322,9 +333,9 @@ def attn_pages_assign(table, lens, new_lens, free_pages, free_count, page_size: 
         if key:
             _keep(key, plan)
     stride, index, B, width, capacity = plan
-    _run(load_library().attn_pages_assign, "attn_pages_assign", index, stream, table.data_ptr(), stride, width,
-         lens.data_ptr(), new_lens.data_ptr(), B, page_size, free_pages.data_ptr(), capacity, free_count.data_ptr(),
-         o["lens"].data_ptr(), o["free_count"].data_ptr(), o["cu"].data_ptr(), o["slots"].data_ptr(),
+    _run(load_library().attn_pages_assign_after, "attn_pages_assign", index, stream, _after(after, index), table.data_ptr(),
+         stride, width, lens.data_ptr(), new_lens.data_ptr(), B, page_size, free_pages.data_ptr(), capacity,
+         free_count.data_ptr(), o["lens"].data_ptr(), o["free_count"].data_ptr(), o["cu"].data_ptr(), o["slots"].data_ptr(),
          o["positions"].data_ptr(), max_tokens, o["info"].data_ptr())
     return o
 

@@ -3,12 +3,15 @@ include/attn.h (argument marshalling only).
 
 A step of a beam search (or of samples that share a prompt) runs
 
-    attn_pages_fork(table, lens, parents, shares, free_pages, free_count, page_size, out=...)
-    moved = attn_pages_own(table, lens, new_lens, shares, free_pages, free_count, page_size, out=...)
+    fork = attn_pages_fork(table, lens, parents, shares, free_pages, free_count, page_size, out=...)
+    moved = attn_pages_own(table, lens, new_lens, shares, free_pages, free_count, page_size, out=..., after=fork["info"])
     attn_pages_copy(cache, moved["src"], moved["dst"])
-    step = attn_pages_assign(table, lens, new_lens, free_pages, free_count, page_size, max_tokens)
+    step = attn_pages_assign(table, lens, new_lens, free_pages, free_count, page_size, max_tokens, after=moved["info"])
 
 and then what serving.py's step runs, without the host knowing a length.
+``after`` carries a refusal forward, so that nothing of the step is done: without it
+the host has to look at attn_pages_own's info before it appends, since a refused
+attn_pages_own leaves pages shared into which attn_pages_assign would put tokens.
 ``shares`` (int32, one per page of the cache, zeros to begin with) counts the
 rows that name a page beyond the first.  Everything else (streams, outputs,
 errors) is as in serving.py.
@@ -16,7 +19,7 @@ errors) is as in serving.py.
 from __future__ import annotations
 
 from .binding import load_library
-from .serving import _I32, _U8, _cuda, _dense, _int_outs, _keep, _page_state, _plans, _rows, _run, _sig, _sizes, _written
+from .serving import _I32, _U8, _after, _cuda, _dense, _int_outs, _keep, _page_state, _plans, _rows, _run, _sig, _sizes, _written
 
 
 def _shared_state(table, lens, arg, arg_name, shares, free_pages, free_count, page_size):
@@ -73,18 +76,21 @@ def release_shared(table, lens, keep_lens, shares, free_pages, free_count, page_
                         shares, free_pages, free_count, page_size, out, stream)
 
 
-def attn_pages_own(table, lens, new_lens, shares, free_pages, free_count, page_size: int, out=None, stream=None) -> dict:
+def attn_pages_own(table, lens, new_lens, shares, free_pages, free_count, page_size: int, out=None, stream=None,
+                   after=None) -> dict:
     """Copy-on-write of the pages that the next attn_pages_assign's tokens go into.
 
     A request with ``new_lens`` > 0 whose last page is partly filled and shared
     gets a page of its own.  ``table`` and ``shares`` are updated in place; returns
-    a dict of free_count [1], src [B], dst [B] (attn_pages_copy's) and info [2]."""
+    a dict of free_count [1], src [B], dst [B] (attn_pages_copy's) and info [2].
+    ``after`` as attn_pages_assign's: attn_pages_fork's info, if the step has one.
+    Refused, it leaves pages shared: give its info to attn_pages_assign."""
     plan, o = _planned("own", 4, table, lens, new_lens, "new_lens", shares, free_pages, free_count, page_size, out, stream,
                        lambda p: {"free_count": 1, "src": p[2], "dst": p[2], "info": 2})
     stride, index, B, width, capacity, pages = plan
-    _run(load_library().attn_pages_own, "attn_pages_own", index, stream, table.data_ptr(), stride, width, lens.data_ptr(),
-         new_lens.data_ptr(), B, page_size, shares.data_ptr(), pages, free_pages.data_ptr(), capacity, free_count.data_ptr(),
-         o["free_count"].data_ptr(), o["src"].data_ptr(), o["dst"].data_ptr(), o["info"].data_ptr())
+    _run(load_library().attn_pages_own_after, "attn_pages_own", index, stream, _after(after, index), table.data_ptr(), stride, width,
+         lens.data_ptr(), new_lens.data_ptr(), B, page_size, shares.data_ptr(), pages, free_pages.data_ptr(), capacity,
+         free_count.data_ptr(), o["free_count"].data_ptr(), o["src"].data_ptr(), o["dst"].data_ptr(), o["info"].data_ptr())
     return o
 
 

@@ -428,7 +428,12 @@ ATTN_API int attn_pages_release(int *block_table, long long table_stride, int ma
  *   from the top of the stack, as if requests were served one after the other (the
  *   last one that names a page keeps it).  src[r] and dst[r] are the old page and
  *   the new one, -1 where nothing changes: attn_pages_copy then copies the contents.
- *   A step is fork, own, copy, assign, append.
+ *   A step is fork, own, copy, assign, append.  A refused own leaves pages shared
+ *   that assign would let tokens into, so the calls of a step are told of one another:
+ * own_after, assign_after  are own and attn_pages_assign, refused with
+ *   AFTER_REFUSAL where `after` (device; the info of the step's call before, which info
+ *   may be) holds a refusal: after[0] is not 0.  A refusal of any call of the step
+ *   then leaves copy without a move and append without a slot.  NULL: as without.
  * compact  renumbers pages so that the used ones are 0 .. num_pages - *free_count - 1:
  *   used pages above take the places of free ones below, both in the order of
  *   their ids.  A page is used unless the stack holds it.  Writes table_out,
@@ -453,7 +458,8 @@ ATTN_API int attn_pages_release(int *block_table, long long table_stride, int ma
  *   BAD_PAGE        an entry that was looked at is not in 0 .. num_pages - 1 (compact:
  *                   or is free, or the stack holds a page twice);
  *   BAD_SHARES      shares has fewer rows for a page than the call found;
- *   TOO_MANY_MOVES  compact: more than max_moves.
+ *   TOO_MANY_MOVES  compact: more than max_moves;
+ *   AFTER_REFUSAL   own_after, assign_after: the call before was refused.
  * shares that are otherwise wrong (negative ones among them) are not found out.
  *
  * lens_out may be lens and free_count_out may be free_count; no other buffers may
@@ -466,6 +472,7 @@ ATTN_API int attn_pages_release(int *block_table, long long table_stride, int ma
 #define ATTN_PAGES_BAD_PAGE 16
 #define ATTN_PAGES_BAD_SHARES 32
 #define ATTN_PAGES_TOO_MANY_MOVES 64
+#define ATTN_PAGES_AFTER_REFUSAL 128
 ATTN_API int attn_pages_fork(int *block_table, long long table_stride, int max_pages, const int *lens,
                              const int *parents, int B, int page_size, int *shares, int num_pages, int *free_pages,
                              int free_capacity, const int *free_count, int *lens_out, int *free_count_out, int *info,
@@ -478,6 +485,15 @@ ATTN_API int attn_pages_own(int *block_table, long long table_stride, int max_pa
                             const int *new_lens, int B, int page_size, int *shares, int num_pages,
                             const int *free_pages, int free_capacity, const int *free_count, int *free_count_out,
                             int *src, int *dst, int *info, attn_stream_t stream);
+ATTN_API int attn_pages_own_after(const int *after, int *block_table, long long table_stride, int max_pages,
+                                  const int *lens, const int *new_lens, int B, int page_size, int *shares,
+                                  int num_pages, const int *free_pages, int free_capacity, const int *free_count,
+                                  int *free_count_out, int *src, int *dst, int *info, attn_stream_t stream);
+ATTN_API int attn_pages_assign_after(const int *after, int *block_table, long long table_stride, int max_pages,
+                                     const int *lens, const int *new_lens, int B, int page_size,
+                                     const int *free_pages, int free_capacity, const int *free_count, int *lens_out,
+                                     int *free_count_out, int *cu, int *slots, int *positions, int max_tokens,
+                                     int *info, attn_stream_t stream);
 ATTN_API int attn_pages_compact(const int *block_table, long long table_stride, int *table_out,
                                 long long table_out_stride, int max_pages, const int *lens, int B, int page_size,
                                 const int *shares, int *shares_out, int num_pages, const int *free_pages,
