@@ -149,7 +149,9 @@ struct Shape {
   static constexpr int V_STEP = kv8_block_bytes(D);  // a block of 16 tokens
   static constexpr int STAGE = K_BYTES + TK / kKv8Block * V_STEP;
   static constexpr int Q_BYTES = NQ * D, P_BYTES = NP * TK;
-  static constexpr int QBUF = D >= 192 && R >= 16 ? 1 : 2;  // Q's buffers: one where it gives K and V a stage
+  // Q's buffers: one where it gives K and V a stage (16 requests of up to 4096, 4 query tokens, D 256: 18.6 us, two
+  // buffers 20.4; 64 of 2000, 16 rows 38 and 46).
+  static constexpr int QBUF = D >= 192 && R >= 16 ? 1 : 2;
   // Of 64 dims (and the second half of 192) the second product multiplies 128 rows
   // all the same: it reads up to 1 KB behind a block, whose results no one reads.
   // Q's and P's buffers lie there.
@@ -160,8 +162,12 @@ struct Shape {
   static constexpr int SMEM = OFF_P + 2 * P_BYTES;
   static constexpr int COLS = 2 * NQ + (TURNS ? 2 : 1) * NH * NP;   // of tensor memory: two tiles' scores, the output
   static constexpr uint32_t TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-  // Warps: softmax, then one that loads, one that multiplies, and those that split Q.
-  static constexpr int WARP_LOAD = GROUPS * 4, WARP_MMA = WARP_LOAD + 1, WARP_Q = WARP_LOAD + 2, Q_WARPS = R == 16 ? 4 : 2;
+  // Warps: softmax, then one that loads, one that multiplies, and those that split Q: two, which leave 168 registers a
+  // thread, but four for 16 rows of many dims. 2 / 4, us: 16 requests of 4 query tokens, D 256, up to 4096 20.2 / 18.6,
+  // of 1365 16.0 / 15.5; 64 of 2730 with 16 rows, D 128 74.4 / 78.5, of 1 to 4096 54.1 / 55.9, 32 of 1000, D 64 24.9 /
+  // 25.5; 28 rows 115 / 174 (spills).
+  static constexpr int WARP_LOAD = GROUPS * 4, WARP_MMA = WARP_LOAD + 1, WARP_Q = WARP_LOAD + 2;
+  static constexpr int Q_WARPS = R == 16 && D >= 192 ? 4 : 2;
   static constexpr int SOFTMAX = GROUPS * 128, AT_TILE = TURNS ? 128 : SOFTMAX, THREADS = (WARP_Q + Q_WARPS) * 32;
   static constexpr int LPR = D == 64 ? 4 : D == 128 ? 8 : 16;  // lanes that split a row, 16 dims each
   static_assert(STAGES >= 2 && COLS <= 512 && STAGE % 16 == 0 && OFF_Q % 128 == 0 && Q_BYTES + P_BYTES >= 1024, "");

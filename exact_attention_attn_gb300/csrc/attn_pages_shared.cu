@@ -759,7 +759,8 @@ int attn_pages_own_after(const int *after, int *block_table, long long table_str
                                                (int)(ATTN_PAGES_MAX_REQUESTS * sizeof(int)));
     if (e != cudaSuccess) return record_cuda_error(e);
   }
-  // (1024 threads for more than 256 rows: then a thread has 16 at most)
+  // 1024 threads for more than 256 rows: then a thread has 16 at most.  256 / 1024 threads, us: 8 rows 3.1 / 4.1, 32 4.4 /
+  // 5.5, 256 5.0 / 6.0.
   attn_pages_own_kernel<<<1, B <= 256 ? 256 : kMaxThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? ATTN_OK : record_cuda_error(e);
