@@ -53,15 +53,18 @@
 // Rows of a tile: the fewest of 4, 8, 16 and (up to 128 dims) 32 that hold a request's
 // rows, or the most there are.  64 requests of 2730 tokens, 8 kv heads of 128, us for
 // tiles of 4 / 8 / 16 / 32 rows:
-//     4 rows 62 / 63 / 72 / 111;  8 rows 101 / 66 / 75 / 113;  12 rows 134 / 106 / 79 / 115;
-//     28 rows 273 / 195 / 139 / 124;  64 rows 593 / 377 / 259 / 219.
+//     4 rows 63 / 63 / 69 / 101;  8 rows 100 / 66 / 70 / 103;  12 rows 134 / 106 / 73 / 105;
+//     28 rows 270 / 195 / 130 / 114;  64 rows 596 / 378 / 244 / 205.
+// The rule goes by T / B, so requests of one call should have about as many query tokens:
+// one of 64 among 63 idle slots takes 46 us (by itself 22), a chunk of 512 beside 63
+// single tokens 192 (apart 107 and 61).
 //
 // Work split.  The tiles of all (request, kv head, row tile) items form one line, an
 // item counting START more for its beginning and end, cut into equal pieces, one a CTA;
 // lengths are read on the device.  START 1 / 2 / 3 / 4: 4 rows, 64 requests of 1 to
-// 8192 tokens 83 / 66 / 67 / 68 us; START 2 / 3 / 4 / 6: 16 rows, 64 of 1 to 4096 65 /
-// 56 / 57 / 60, of D 256 (16 requests) 19.7 / 20.1 / 18.6 / 18.4, 28 rows 109 / 95 / 90
-// / 86.  A cut item's parts go to a workspace and are merged by a second kernel in the
+// 8192 tokens 83 / 66 / 67 / 68 us; START 2 / 3 / 4 / 6: 16 rows, 64 of 1 to 4096 55 /
+// 53 / 54 / 57, of D 256 (16 requests) 19.6 / 19.5 / 18.6 / 18.4, 28 rows 94 / 85 / 78
+// / 80.  A cut item's parts go to a workspace and are merged by a second kernel in the
 // order of the tokens.  Few and short items have a cluster of CTAs each instead, merged
 // through distributed shared memory (the rule and its figures: launch_kv8).
 //
@@ -72,8 +75,9 @@
 // first tile and the merge (4 us).  D 256 63 (53); 16 requests of up to 4096 with 4
 // query tokens 18.6 (7): that latency alone.  D 64 45 (27): a tile's 16 KB arrive
 // faster than one warp issues its copies and one its products (about 800 clocks a tile
-// each). 64 of 2730 with 16 rows 80, with 28 122 (53): the softmax's arithmetic, every
-// weight split in four.  One request of 129 tokens 6.3.
+// each). 64 of 2730 with 16 rows 74, with 28 115 (53): the softmax's chain (every weight
+// split in four), of which an SM holds two warps a scheduler: they issue in 0.39 of the
+// clocks.  One request of 129 tokens 6.2.
 #include <cuda_bf16.h>
 #include <float.h>
 #include <math.h>
@@ -1385,15 +1389,15 @@ int launch_kv8(Kv8Params &p, int device, int sms, cudaStream_t st) {
   const int64_t by_rows = (int64_t)p.T * p.group / S::R + p.B, by_token = (int64_t)p.T * ((p.group + S::R - 1) / S::R);
   const int64_t tiles = (((int64_t)p.max_pages << p.shift) + TK - 1) / TK;
   const int64_t items = (by_rows < by_token ? by_rows : by_token) * p.H;
-  if (items > ((int64_t)1 << 40) / (tiles + 1 + S::START)) return ATTN_ERR_ARG;  // a piece's units are 32-bit
+  if (items > ((int64_t)1 << 40) / (tiles + 1 + S::START)) return ATTN_ERR_ARG;  // the line's units: far inside 64 bits
   // Few and short items have a cluster of CTAs each (a power of two up to 8, doubled while a CTA has more than two
   // tiles and all clusters are resident at once), and no second kernel; pieces spread the tiles over all SMs, but
   // cost the merge's launch and about kMergeTiles tiles' time more.  The lengths are taken to be half of what the
   // table allows on average: a cluster waits for the longest.  Requests x tokens (D 128, 8 kv heads), pieces ->
-  // clusters, us: 1 x 500 9.7 -> 7.3, 1 x 4000 11.0 -> 9.5, 1 x 8000 11.3 -> 12.0, 1 x 16000 13.2 -> 17.7, 4 x 4000
-  // 14.3 -> 12.4, 8 x 2000 14.7 -> 12.3, 16 x 1000 15.8 -> 11.3, 16 x 2000 20.3 -> 16.7; 16 ragged ones of up to
-  // 4096, D 256: 20 -> 38.  Doubled down to one tile a CTA, one request of 129 tokens 6.4 -> 6.9 us; three or four
-  // left, 1 x 1000 7.9 -> 9.1.
+  // clusters, us: 1 x 500 9.3 -> 7.5, 1 x 4000 10.5 -> 9.1, 1 x 8000 10.9 -> 11.5, 1 x 16000 12.9 -> 16.6, 8 x 2000
+  // 13.8 -> 12.0 (ragged, up to 2000: 12.0 both), 16 x 1000 15.0 -> 10.8; 4 x 4000 13.7 -> 12.1 and 16 x 2000 18.8 ->
+  // 15.6 have pieces all the same, as ragged ones take 11.1 -> 12.1 and 14.0 -> 15.6 (16 of up to 4000: 16.5 -> 25.2).
+  // Doubled down to one tile a CTA, one request of 129 tokens 6.4 -> 6.9 us; three or four left, 1 x 1000 7.9 -> 9.1.
   p.cluster = 1;
   for (int i = 0; i < kClusterSizes && tiles > 2 * p.cluster && items <= held[i]; ++i) p.cluster *= 2;
   if (items <= sms && (tiles + p.cluster - 1) / p.cluster <= items * (tiles / 2 + S::START) / sms + kMergeTiles) {

@@ -18,8 +18,8 @@
 // token only, the K and V of two heads in flight.
 //
 // Measured: append of 16384 tokens of 8 heads of 128 (101 MB) 20.0 us, 5.0 TB/s, bound
-// by instruction issue and by its latency (128 registers for the block's words, 16
-// warps an SM; 3 or 4 CTAs an SM spill: 26 .. 44 us).  Read of them 16.5 us, 6.1 TB/s:
+// by the latency of its loads (a lane has 32 registers of the block's words under way, 116
+// of the 128 that two CTAs an SM leave, so 16 warps; 3 or 4 CTAs spill: 26 .. 44 us).  Read of them 16.5 us, 6.1 TB/s:
 // HBM. Append of 64 single tokens 3.2 us, three dependent loads; of 1024 17.5 us (20 as
 // blocks): a token's V is a byte in each of D rows of 16, so what is written are
 // partial sectors.

@@ -654,18 +654,23 @@ ATTN_API int attn_kv8_read(const void *cache, int num_pages, const int *slots, v
  * 2^-28 of the largest such product of the row, whichever is coarser.  O is rounded
  * once to bf16.
  *        Ranges: |q| scale and K up to 2^100 each, their scores below 2^127 in
- *        magnitude; V any finite bf16.  Scores of any size leave O's error as it is
- *        where the tokens' scores are equal or far apart.  A marked token makes NaN what sees it: K's mark O and
- *        LSE, V's O.  Scales must be powers of two, from 2^-100 to 2^120, as
- *        attn_kv8_append makes them.
+ *        magnitude; V any finite bf16.  Where the scores are equal or far apart, O's
+ *        error does not grow with them.  A marked token makes NaN what sees it: K's
+ *        mark O and LSE, V's O.  Scales must be powers of two, from 2^-100 to 2^120,
+ *        as attn_kv8_append makes them.
  * D      64, 128, 192 or 256.  max_pages * page_size < 2^31 - 1024.
- * Nothing in a page past a request's last token, and nothing hidden from a row,
- * reaches that row's result, whatever it holds.  Table entries, lengths and query
- * tokens out of range, and a cu that descends: as attn_fwd_kv4.
+ * Nothing in a page past a request's last token reaches a result, whatever it
+ * holds, and no number, scale or mark of a token hidden from a row reaches that
+ * row's (a NaN among a token's codes, which attn_kv8_append never writes, may).
+ * Requests of one call should have about as many query tokens each: tiles are
+ * chosen by T / B, and much other counts cost time.  (T * Hq / Hkv + B) * Hkv *
+ * (max_pages * page_size / 128 + 6) below 2^40 is always taken, far larger calls are
+ * refused with ATTN_ERR_ARG.  Table entries, lengths and query tokens out of range,
+ * and a cu that descends: as attn_fwd_kv4.
  *
  * Asynchronous on `stream`: one launch (a thread-block cluster for each item) where
  * items and the table are few and short, by the sizes alone; else two launches
- * and a stream-ordered workspace of at most 5.1 MB (152 SMs) from the library's pool
+ * and a stream-ordered workspace of at most 5.2 MB (152 SMs) from the library's pool
  * (ATTN_ERR_NOMEM if it cannot be had).  CUDA graphs: as attn_fwd; the grid depends
  * on the sizes alone, so a replay may have other lengths, tables and query counts.
  * Device-side waits are bounded (attn_fwd_status: ATTN_ERR_TIMEOUT).  Deterministic
